@@ -199,6 +199,103 @@ BITNET_API int bitnet_w2a8_gemm_noalloc(const int8_t *q, const uint8_t *packed, 
                                         int64_t N, int64_t K, void *stream);
 
 /*
+ * ------------------------------------------------------------------ 4-bit floating point
+ * Microscaled 4-bit floating point, for the layers that are not ternary (the
+ * pages have no counterpart).  Elements are e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ * and their negatives (codes 0..7, bit 3 the sign).  Two formats:
+ *   BITNET_FP4_MX  blocks of 32 along K share an e8m0 scale 2^(byte - 127)
+ *   BITNET_FP4_NV  blocks of 16 along K share an e4m3 scale
+ * and, with either, an optional fp32 tensor scale g (NULL = 1).  A matrix
+ * [rows, K] is stored as
+ *   codes   rows of K_pad / 2 bytes, K_pad = 128 * ceil(K / 128); the even k of
+ *           a byte in its low half; K <= k < K_pad holds code 0
+ *   scales  tiles of 128 rows x 4 blocks, 512 bytes: row r and block c of a tile
+ *           at byte 16 * (r mod 32) + 4 * (r / 32) + c; the tiles of a 128-row
+ *           band follow one another (K_pad / 128 of them for MX, K_pad / 64 for
+ *           NV), then the next band; rows past the matrix hold byte 0
+ * and stands for element * scale * g.
+ */
+enum { BITNET_FP4_MX = 0, BITNET_FP4_NV = 1 };
+
+/* Types of x and y. */
+enum { BITNET_BF16 = 0, BITNET_FP16 = 1, BITNET_FP32 = 2 };
+
+/* Bytes of the codes and of the scales of a [rows, K] matrix, or -1 for
+ * invalid sizes or an unknown format. */
+BITNET_API int64_t bitnet_fp4_code_bytes(int64_t rows, int64_t K);
+BITNET_API int64_t bitnet_fp4_scale_bytes(int64_t rows, int64_t K, int format);
+
+/*
+ * Workspace bytes that bitnet_fp4_tensor_scale (M = its rows), bitnet_fp4_gemm
+ * and bitnet_fp4_linear need for an M x N x K problem (the maximum over the
+ * three), or -1 for invalid sizes or an unknown format.  Depends only on its
+ * arguments.
+ */
+BITNET_API int64_t bitnet_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K, int format);
+
+/*
+ * Tensor scale: g = max(fl32(max |x| / 2688), 2^-126) over the finite values
+ * of x (2688 = 6 * 448, the largest value of the NV format at g = 1).
+ *   x         device, dtype [rows, K], row stride ldx >= K elements, aligned to
+ *             its element
+ *   g         device, 1 float (output)
+ *   workspace device, >= bitnet_fp4_workspace_bytes(rows, 1, K, format) bytes,
+ *             256-byte aligned
+ */
+BITNET_API int bitnet_fp4_tensor_scale(const void *x, int dtype, int64_t rows, int64_t K, int64_t ldx, float *g,
+                                       void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Quantisation.  z = fl32(x * fl32(1 / g)); per block, with top = max |z|,
+ *   MX  scale 2^(floor(log2 top) - 2) (never below 2^-127)
+ *   NV  scale e4m3(fl32(top / 6)), to nearest even, at most 448
+ *   code = e2m1(z / scale), to nearest even, at most 6 (0 for a zero scale).
+ * A block with a NaN or an infinity gets a NaN scale (MX 255, NV 127) and
+ * codes 0, so that products with it are NaN.
+ *   x      as in bitnet_fp4_tensor_scale
+ *   g      device, 1 float > 0, or NULL
+ *   codes  device, bitnet_fp4_code_bytes(rows, K) bytes, 16-byte aligned (output)
+ *   scales device, bitnet_fp4_scale_bytes(rows, K, format) bytes, 16-byte
+ *          aligned (output)
+ */
+BITNET_API int bitnet_fp4_quant(const void *x, int dtype, int64_t rows, int64_t K, int64_t ldx, int format,
+                                const float *g, uint8_t *codes, uint8_t *scales, void *stream);
+
+/*
+ * Reading back: y[r, k] = round(fl32(element * scale) * g), one rounding to
+ * the type of y after one in fp32.
+ *   y  device, dtype [rows, K], row stride ldy >= K elements (output)
+ */
+BITNET_API int bitnet_fp4_dequant(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t K, int format,
+                                  const float *g, void *y, int dtype, int64_t ldy, void *stream);
+
+/*
+ * Product of two quantised matrices of the same format:
+ *   y[m, n] = round(ga * gw * sum_k A[m, k] * W[n, k]),
+ * A and W the values without their tensor scales, summed in fp32 (the order
+ * and the grouping of the sums depend on the sizes only).
+ *   a, a_scales  A [M, K];  w, w_scales  W [N, K];  all 16-byte aligned
+ *   ga, gw       device, 1 float each, or NULL
+ *   y            device, dtype BITNET_BF16 or BITNET_FP16 [M, N], row stride
+ *                ldy >= N elements (output)
+ *   workspace    device, >= bitnet_fp4_workspace_bytes(M, N, K, format) bytes,
+ *                256-byte aligned
+ */
+BITNET_API int bitnet_fp4_gemm(const uint8_t *a, const uint8_t *a_scales, const float *ga, const uint8_t *w,
+                               const uint8_t *w_scales, const float *gw, int format, void *y, int dtype, int64_t M,
+                               int64_t N, int64_t K, int64_t ldy, void *workspace, int64_t workspace_bytes,
+                               void *stream);
+
+/*
+ * Linear layer: quantises x with the tensor scale ga, then the product above;
+ * the values are those of bitnet_fp4_quant followed by bitnet_fp4_gemm.
+ */
+BITNET_API int bitnet_fp4_linear(const void *x, int xdtype, int64_t ldx, const float *ga, const uint8_t *w,
+                                 const uint8_t *w_scales, const float *gw, int format, void *y, int ydtype, int64_t M,
+                                 int64_t N, int64_t K, int64_t ldy, void *workspace, int64_t workspace_bytes,
+                                 void *stream);
+
+/*
  * Device-side error word.  Kernels whose threads wait on one another bound
  * every wait; a wait that runs out records BITNET_ERR_DEVICE_TIMEOUT in a
  * per-device word (the kernel then stops and leaves its output incomplete).

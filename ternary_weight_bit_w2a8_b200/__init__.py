@@ -23,9 +23,16 @@ BITNET_ERR_CUDA = 4
 BITNET_ERR_DEVICE_TIMEOUT = 5
 BITNET_ERR_UNSUPPORTED = 6
 
+BITNET_FP4_MX = 0  # blocks of 32, e8m0 scales
+BITNET_FP4_NV = 1  # blocks of 16, e4m3 scales
+BITNET_BF16 = 0
+BITNET_FP16 = 1
+BITNET_FP32 = 2
+
 _lib = None
 
 _i64 = ctypes.c_int64
+_int = ctypes.c_int
 _p = ctypes.c_void_p
 _SIGNATURES = {
     "bitnet_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -39,6 +46,15 @@ _SIGNATURES = {
     "bitnet_w2a8_gemm": (ctypes.c_int, [_p, _p, _p, _i64, _i64, _i64, _p, _i64, _p]),
     "bitnet_bitlinear": (ctypes.c_int, [_p, _p, _p, _p, _i64, _i64, _i64, _p, _i64, _p]),
     "bitnet_w2a8_gemm_noalloc": (ctypes.c_int, [_p, _p, _p, _i64, _i64, _i64, _p]),
+    "bitnet_fp4_code_bytes": (_i64, [_i64, _i64]),
+    "bitnet_fp4_scale_bytes": (_i64, [_i64, _i64, _int]),
+    "bitnet_fp4_workspace_bytes": (_i64, [_i64, _i64, _i64, _int]),
+    "bitnet_fp4_tensor_scale": (ctypes.c_int, [_p, _int, _i64, _i64, _i64, _p, _p, _i64, _p]),
+    "bitnet_fp4_quant": (ctypes.c_int, [_p, _int, _i64, _i64, _i64, _int, _p, _p, _p, _p]),
+    "bitnet_fp4_dequant": (ctypes.c_int, [_p, _p, _i64, _i64, _int, _p, _p, _int, _i64, _p]),
+    "bitnet_fp4_gemm": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _int, _p, _int, _i64, _i64, _i64, _i64, _p, _i64, _p]),
+    "bitnet_fp4_linear": (ctypes.c_int, [_p, _int, _i64, _p, _p, _p, _p, _int, _p, _int, _i64, _i64, _i64, _i64, _p,
+                                         _i64, _p]),
     "bitnet_get_device_error": (ctypes.c_int, [_p]),
     "bitnet_launch_count": (_i64, []),
 }
@@ -217,6 +233,188 @@ def bitnet_w2a8_gemm_noalloc(q, packed, N: int, y=None, stream=None):
         y = torch.empty((M, N), dtype=torch.int32, device=q.device)
     _check(lib().bitnet_w2a8_gemm_noalloc(_ptr(q), _ptr(packed), _ptr(y), M, N, K, _stream(stream)),
            "bitnet_w2a8_gemm_noalloc")
+    return y
+
+
+# ------------------------------------------------------------------ 4-bit floating point
+# The matrices here may lie on any one CUDA device (it is made current for the
+# call); x and y may be row-strided views, everything else is contiguous.
+
+def _fp4_dtype(t, name="x"):
+    import torch
+    d = {torch.bfloat16: BITNET_BF16, torch.float16: BITNET_FP16, torch.float32: BITNET_FP32}.get(t)
+    if d is None:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32")
+    return d
+
+
+def _rows(t, name, device=None):
+    """(rows, columns, row stride) of a 2-D CUDA tensor whose rows are contiguous."""
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be a CUDA tensor on the call's device")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with contiguous rows")
+    rows, cols = t.shape
+    return rows, cols, (t.stride(0) if rows > 1 else cols)
+
+
+def _plain(t, name, dtype, device, numel):
+    if t is None:
+        return
+    if not t.is_cuda or t.device != device or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor on the call's device")
+    if t.numel() < numel:
+        raise ValueError(f"{name} holds {t.numel()} elements, {numel} are needed")
+
+
+def _fp4_matrix(codes, scales, K, fmt, device, name):
+    """Rows of a quantised matrix whose codes are [rows, K_pad / 2]."""
+    import torch
+    if codes.dim() != 2 or codes.shape[1] != bitnet_fp4_code_bytes(1, K):
+        raise ValueError(f"{name} must be [rows, {bitnet_fp4_code_bytes(1, K)}] for K = {K}")
+    rows = codes.shape[0]
+    _plain(codes, name, torch.uint8, device, 0)
+    _plain(scales, f"{name}'s scales", torch.uint8, device, bitnet_fp4_scale_bytes(rows, K, fmt))
+    return rows
+
+
+class _on:
+    """Makes `device` and, where given, `stream` current: what the call
+    allocates belongs to the stream that it runs on."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.device = torch.cuda.device(device)
+        self.stream = torch.cuda.stream(stream) if stream is not None else None
+
+    def __enter__(self):
+        self.device.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+        return _stream()
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        self.device.__exit__(*exc)
+
+
+def _fp4_workspace(ws, need, device):
+    import torch
+    if ws is None:
+        return torch.empty(max(256, need), dtype=torch.uint8, device=device)
+    _plain(ws, "ws", torch.uint8, device, 0)
+    return ws
+
+
+def bitnet_fp4_code_bytes(rows: int, K: int) -> int:
+    n = lib().bitnet_fp4_code_bytes(rows, K)
+    if n < 0:
+        raise BitnetError(BITNET_ERR_INVALID_ARG, "bitnet_fp4_code_bytes")
+    return n
+
+
+def bitnet_fp4_scale_bytes(rows: int, K: int, fmt: int) -> int:
+    n = lib().bitnet_fp4_scale_bytes(rows, K, fmt)
+    if n < 0:
+        raise BitnetError(BITNET_ERR_INVALID_ARG, "bitnet_fp4_scale_bytes")
+    return n
+
+
+def bitnet_fp4_workspace_bytes(M: int, N: int, K: int, fmt: int) -> int:
+    n = lib().bitnet_fp4_workspace_bytes(M, N, K, fmt)
+    if n < 0:
+        raise BitnetError(BITNET_ERR_INVALID_ARG, "bitnet_fp4_workspace_bytes")
+    return n
+
+
+def bitnet_fp4_tensor_scale(x, g=None, ws=None, stream=None):
+    """Tensor scale of the NV format, max|x| / 2688 over the finite values of x -> float32 tensor [1]."""
+    import torch
+    rows, K, ldx = _rows(x, "x")
+    with _on(x.device, stream) as st:
+        if g is None:
+            g = torch.empty(1, dtype=torch.float32, device=x.device)
+        _plain(g, "g", torch.float32, x.device, 1)
+        ws = _fp4_workspace(ws, bitnet_fp4_workspace_bytes(rows, 1, K, BITNET_FP4_NV) if ws is None else 0, x.device)
+        _check(lib().bitnet_fp4_tensor_scale(_ptr(x), _fp4_dtype(x.dtype), rows, K, ldx, _ptr(g), _ptr(ws), ws.numel(),
+                                             st), "bitnet_fp4_tensor_scale")
+    return g
+
+
+def bitnet_fp4_quant(x, fmt: int, g=None, codes=None, scales=None, stream=None):
+    """Quantises x [rows, K] -> (codes uint8 [rows, K_pad / 2], scales uint8 [bitnet_fp4_scale_bytes(rows, K, fmt)])."""
+    import torch
+    rows, K, ldx = _rows(x, "x")
+    with _on(x.device, stream) as st:
+        if codes is None:
+            codes = torch.empty((rows, bitnet_fp4_code_bytes(1, K)), dtype=torch.uint8, device=x.device)
+        if scales is None:
+            scales = torch.empty(bitnet_fp4_scale_bytes(rows, K, fmt), dtype=torch.uint8, device=x.device)
+        if _fp4_matrix(codes, scales, K, fmt, x.device, "codes") != rows:
+            raise ValueError("codes and x differ in their rows")
+        _plain(g, "g", torch.float32, x.device, 1)
+        _check(lib().bitnet_fp4_quant(_ptr(x), _fp4_dtype(x.dtype), rows, K, ldx, fmt, _ptr(g), _ptr(codes),
+                                      _ptr(scales), st), "bitnet_fp4_quant")
+    return codes, scales
+
+
+def bitnet_fp4_dequant(codes, scales, K: int, fmt: int, g=None, dtype=None, y=None, stream=None):
+    """The values of a quantised matrix -> y [rows, K] (bfloat16 unless dtype or y says otherwise)."""
+    import torch
+    rows = _fp4_matrix(codes, scales, K, fmt, codes.device, "codes")
+    with _on(codes.device, stream) as st:
+        if y is None:
+            y = torch.empty((rows, K), dtype=dtype or torch.bfloat16, device=codes.device)
+        yr, yk, ldy = _rows(y, "y", codes.device)
+        if (yr, yk) != (rows, K):
+            raise ValueError(f"y must be [{rows}, {K}]")
+        _plain(g, "g", torch.float32, codes.device, 1)
+        _check(lib().bitnet_fp4_dequant(_ptr(codes), _ptr(scales), rows, K, fmt, _ptr(g), _ptr(y),
+                                        _fp4_dtype(y.dtype, "y"), ldy, st), "bitnet_fp4_dequant")
+    return y
+
+
+def bitnet_fp4_gemm(a, a_scales, w, w_scales, K: int, fmt: int, ga=None, gw=None, dtype=None, y=None, ws=None,
+                    stream=None):
+    """y = A W^T of quantised A [M, K] and W [N, K] -> [M, N] (bfloat16 or float16)."""
+    import torch
+    dev = a.device
+    M = _fp4_matrix(a, a_scales, K, fmt, dev, "a")
+    N = _fp4_matrix(w, w_scales, K, fmt, dev, "w")
+    with _on(dev, stream) as st:
+        if y is None:
+            y = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=dev)
+        ym, yn, ldy = _rows(y, "y", dev)
+        if (ym, yn) != (M, N):
+            raise ValueError(f"y must be [{M}, {N}]")
+        _plain(ga, "ga", torch.float32, dev, 1)
+        _plain(gw, "gw", torch.float32, dev, 1)
+        ws = _fp4_workspace(ws, bitnet_fp4_workspace_bytes(M, N, K, fmt) if ws is None else 0, dev)
+        _check(lib().bitnet_fp4_gemm(_ptr(a), _ptr(a_scales), _ptr(ga), _ptr(w), _ptr(w_scales), _ptr(gw), fmt,
+                                     _ptr(y), _fp4_dtype(y.dtype, "y"), M, N, K, ldy, _ptr(ws), ws.numel(), st),
+               "bitnet_fp4_gemm")
+    return y
+
+
+def bitnet_fp4_linear(x, w, w_scales, fmt: int, ga=None, gw=None, dtype=None, y=None, ws=None, stream=None):
+    """y = quantised(x) W^T: x [M, K] of any type, quantised W [N, K] -> [M, N] (bfloat16 or float16)."""
+    import torch
+    dev = x.device
+    M, K, ldx = _rows(x, "x")
+    N = _fp4_matrix(w, w_scales, K, fmt, dev, "w")
+    with _on(dev, stream) as st:
+        if y is None:
+            y = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=dev)
+        ym, yn, ldy = _rows(y, "y", dev)
+        if (ym, yn) != (M, N):
+            raise ValueError(f"y must be [{M}, {N}]")
+        _plain(ga, "ga", torch.float32, dev, 1)
+        _plain(gw, "gw", torch.float32, dev, 1)
+        ws = _fp4_workspace(ws, bitnet_fp4_workspace_bytes(M, N, K, fmt) if ws is None else 0, dev)
+        _check(lib().bitnet_fp4_linear(_ptr(x), _fp4_dtype(x.dtype), ldx, _ptr(ga), _ptr(w), _ptr(w_scales), _ptr(gw),
+                                       fmt, _ptr(y), _fp4_dtype(y.dtype, "y"), M, N, K, ldy, _ptr(ws), ws.numel(), st),
+               "bitnet_fp4_linear")
     return y
 
 

@@ -8,8 +8,11 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
+#include "fp4.cuh"
+#include "fp4_gemm.cuh"
 #include "gemv.cuh"
 #include "gemv_tma.cuh"
 #include "gemm_tc.cuh"
@@ -921,6 +924,103 @@ int run_w2a8_gemm(DeviceInfo *dev, const int8_t *q, const uint8_t *packed, int32
     return launch_gemm_tc(dev, qa, lda, packed, M, N, K, y, nullptr, nullptr, nullptr, p.tc, p.tc.S > 1, st);
 }
 
+// ------------------------------------------------------------------ 4-bit floating point
+inline bool fp4_format_ok(int f) { return f == BITNET_FP4_MX || f == BITNET_FP4_NV; }
+inline bool fp4_dtype_ok(int t) { return t == BITNET_BF16 || t == BITNET_FP16 || t == BITNET_FP32; }
+inline int fp4_dtype_size(int t) { return t == BITNET_FP32 ? 4 : 2; }
+inline bool fp4_ld_ok(int64_t rows, int64_t cols, int64_t ld) { return ld >= cols && (rows <= 1 || ld <= ((int64_t)1 << 60) / rows); }
+
+// Calls f with the type (and the format) as constants.
+template <typename F>
+int fp4_by_type(int dtype, F f) {
+    switch (dtype) {
+        case BITNET_BF16: return f(std::integral_constant<int, BITNET_BF16>{});
+        case BITNET_FP16: return f(std::integral_constant<int, BITNET_FP16>{});
+        default: return f(std::integral_constant<int, BITNET_FP32>{});
+    }
+}
+template <typename F>
+int fp4_by_format(int format, F f) {
+    if (format == BITNET_FP4_MX) return f(std::integral_constant<int, BITNET_FP4_MX>{});
+    return f(std::integral_constant<int, BITNET_FP4_NV>{});
+}
+
+inline int64_t fp4_patches(int64_t rows, int64_t K) {
+    return ceil_div(rows, kFp4TileRows) * ceil_div(k_pad(K), kFp4PatchK);
+}
+
+int launch_fp4_quant(const void *x, int dtype, int64_t rows, int64_t K, int64_t ldx, int format, const float *g,
+                     uint8_t *codes, uint8_t *scales, cudaStream_t st) {
+    return fp4_by_type(dtype, [&](auto dt) {
+        return fp4_by_format(format, [&](auto fm) {
+            using T = typename Fp4Type<decltype(dt)::value>::T;
+            return launched(launch_pdl(fp4_quant_kernel<decltype(dt)::value, decltype(fm)::value>,
+                                       dim3((unsigned)fp4_patches(rows, K)), dim3(kThreads), (size_t)0, st,
+                                       static_cast<const T *>(x), rows, K, ldx, g, codes, scales));
+        });
+    });
+}
+
+template <int FMT, int BT, int DT>
+int launch_fp4_gemm_variant(DeviceInfo *dev, const CUtensorMap &pmap, const CUtensorMap &qmap, const Fp4GemmArgs &a,
+                            cudaStream_t st) {
+    (void)dev;
+    auto kern = fp4_gemm_kernel<FMT, BT, DT>;
+    constexpr size_t smem = Fp4Smem<FMT, BT>::kBytes + 1024;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return BITNET_ERR_CUDA;
+    const int64_t units = (int64_t)a.tiles_p * ceil_div(a.Q, BT);
+    if (units > (int64_t)1 << 30) return BITNET_ERR_UNSUPPORTED;
+    return launched(launch_pdl(kern, dim3((unsigned)units), dim3(kFp4Threads), smem, st, pmap, qmap, a));
+}
+
+int launch_fp4_gemm(DeviceInfo *dev, const uint8_t *a, const uint8_t *sa, const float *ga, const uint8_t *w,
+                    const uint8_t *sw, const float *gw, int format, void *y, int dtype, int64_t M, int64_t N, int64_t K,
+                    int64_t ldy, cudaStream_t st) {
+    if (tensor_map_encoder() == nullptr) return BITNET_ERR_CUDA;
+    // few tokens: the weights are the P operand and the tokens one tile of Q
+    const bool tokens_q = M <= 128;
+    const int BT = M <= 16 ? 16 : (M <= 64 ? 64 : 128);
+    Fp4GemmArgs g{};
+    const uint8_t *p = tokens_q ? w : a, *q = tokens_q ? a : w;
+    g.sp = tokens_q ? sw : sa;
+    g.sq = tokens_q ? sa : sw;
+    g.P = tokens_q ? N : M;
+    g.Q = tokens_q ? M : N;
+    g.K = K;
+    g.stride_p = tokens_q ? 1 : ldy;
+    g.stride_q = tokens_q ? ldy : 1;
+    g.ga = ga;
+    g.gw = gw;
+    g.y = y;
+    g.tiles_p = (int)ceil_div(g.P, kFp4Rows);
+    const uint64_t rb = (uint64_t)fp4_row_bytes(K);
+    CUtensorMap pmap, qmap;
+    if (!encode_2d(&pmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, rb, (uint64_t)g.P, rb, 128, kFp4Rows,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
+        !encode_2d(&qmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, rb, (uint64_t)g.Q, rb, 128, (uint32_t)BT,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
+        return BITNET_ERR_CUDA;
+    return fp4_by_format(format, [&](auto fm) {
+        constexpr int F = decltype(fm)::value;
+        auto by_bt = [&](auto bt) {
+            constexpr int B = decltype(bt)::value;
+            if (dtype == BITNET_FP16) return launch_fp4_gemm_variant<F, B, BITNET_FP16>(dev, pmap, qmap, g, st);
+            return launch_fp4_gemm_variant<F, B, BITNET_BF16>(dev, pmap, qmap, g, st);
+        };
+        if (BT == 16) return by_bt(std::integral_constant<int, 16>{});
+        if (BT == 64) return by_bt(std::integral_constant<int, 64>{});
+        return by_bt(std::integral_constant<int, 128>{});
+    });
+}
+
+// y = 0 (K == 0).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) fp4_zero_kernel(T *y, int64_t rows, int64_t cols, int64_t ldy) {
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < rows * cols; i += (int64_t)gridDim.x * kThreads)
+        y[i / cols * ldy + i % cols] = T(0.0f);
+}
+
 inline bool q_tma_ok(const int8_t *q, int64_t K) { return (K % 16) == 0 && aligned(q, 16); }
 
 }  // namespace
@@ -1117,6 +1217,146 @@ BITNET_API int bitnet_w2a8_gemm_noalloc(const int8_t *q, const uint8_t *packed, 
         return launched();
     }
     return run_w2a8_gemm(dev, q, packed, y, M, N, K, scratch, p, st);
+}
+
+BITNET_API int64_t bitnet_fp4_code_bytes(int64_t rows, int64_t K) {
+    if (!sizes_ok(rows, 1, K)) return -1;
+    return rows * fp4_row_bytes(K);
+}
+
+BITNET_API int64_t bitnet_fp4_scale_bytes(int64_t rows, int64_t K, int format) {
+    if (!sizes_ok(rows, 1, K) || !fp4_format_ok(format)) return -1;
+    return ceil_div(rows, kFp4TileRows) * fp4_scale_tiles(K, format) * kFp4TileBytes;
+}
+
+BITNET_API int64_t bitnet_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K, int format) {
+    if (!sizes_ok(M, 1, K) || !sizes_ok(N, 1, K) || !fp4_format_ok(format)) return -1;
+    const int64_t scale = (int64_t)kFp4ScaleMaxBlocks * 4;
+    const int64_t linear = round_up(bitnet_fp4_code_bytes(M, K), 256) + round_up(bitnet_fp4_scale_bytes(M, K, format), 256);
+    return linear > scale ? linear : scale;
+}
+
+BITNET_API int bitnet_fp4_tensor_scale(const void *x, int dtype, int64_t rows, int64_t K, int64_t ldx, float *g,
+                                       void *workspace, int64_t workspace_bytes, void *stream) {
+    if (!sizes_ok(rows, 1, K) || !fp4_dtype_ok(dtype) || !fp4_ld_ok(rows, K, ldx) || g == nullptr ||
+        (rows * K > 0 && x == nullptr))
+        return BITNET_ERR_INVALID_ARG;
+    if (!aligned(x, fp4_dtype_size(dtype)) || !aligned(g, 4)) return BITNET_ERR_ALIGNMENT;
+    if (workspace == nullptr || workspace_bytes < (int64_t)kFp4ScaleMaxBlocks * 4) return BITNET_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return BITNET_ERR_ALIGNMENT;
+    DeviceInfo *dev = nullptr;
+    int rc = device_info(&dev);
+    if (rc != BITNET_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    uint32_t *partial = static_cast<uint32_t *>(workspace);
+    int64_t blocks = ceil_div(rows * ceil_div(K, 8), kThreads);
+    if (blocks > kFp4ScaleMaxBlocks) blocks = kFp4ScaleMaxBlocks;
+    if (blocks > 0) {
+        rc = fp4_by_type(dtype, [&](auto dt) {
+            using T = typename Fp4Type<decltype(dt)::value>::T;
+            return launched(launch_pdl(fp4_absmax_kernel<decltype(dt)::value>, dim3((unsigned)blocks), dim3(kThreads),
+                                       (size_t)0, st, static_cast<const T *>(x), rows, K, ldx, partial));
+        });
+        if (rc != BITNET_OK) return rc;
+    }
+    return launched(launch_pdl(fp4_tensor_scale_kernel, dim3(1), dim3(kThreads), (size_t)0, st,
+                               (const uint32_t *)partial, (int)blocks, g));
+}
+
+BITNET_API int bitnet_fp4_quant(const void *x, int dtype, int64_t rows, int64_t K, int64_t ldx, int format,
+                                const float *g, uint8_t *codes, uint8_t *scales, void *stream) {
+    if (!sizes_ok(rows, 1, K) || !fp4_dtype_ok(dtype) || !fp4_format_ok(format) || !fp4_ld_ok(rows, K, ldx))
+        return BITNET_ERR_INVALID_ARG;
+    if (rows * K == 0) return BITNET_OK;
+    if (x == nullptr || codes == nullptr || scales == nullptr) return BITNET_ERR_INVALID_ARG;
+    if (!aligned(x, fp4_dtype_size(dtype)) || !aligned(g, 4) || !aligned(codes, 16) || !aligned(scales, 16))
+        return BITNET_ERR_ALIGNMENT;
+    if (fp4_patches(rows, K) > (1LL << 31) - 1) return BITNET_ERR_UNSUPPORTED;
+    DeviceInfo *dev = nullptr;
+    const int rc = device_info(&dev);
+    if (rc != BITNET_OK) return rc;
+    return launch_fp4_quant(x, dtype, rows, K, ldx, format, g, codes, scales, static_cast<cudaStream_t>(stream));
+}
+
+BITNET_API int bitnet_fp4_dequant(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t K, int format,
+                                  const float *g, void *y, int dtype, int64_t ldy, void *stream) {
+    if (!sizes_ok(rows, 1, K) || !fp4_dtype_ok(dtype) || !fp4_format_ok(format) || !fp4_ld_ok(rows, K, ldy))
+        return BITNET_ERR_INVALID_ARG;
+    if (rows * K == 0) return BITNET_OK;
+    if (y == nullptr || codes == nullptr || scales == nullptr) return BITNET_ERR_INVALID_ARG;
+    if (!aligned(y, fp4_dtype_size(dtype)) || !aligned(g, 4) || !aligned(codes, 16) || !aligned(scales, 16))
+        return BITNET_ERR_ALIGNMENT;
+    if (fp4_patches(rows, K) > (1LL << 31) - 1) return BITNET_ERR_UNSUPPORTED;
+    DeviceInfo *dev = nullptr;
+    const int rc = device_info(&dev);
+    if (rc != BITNET_OK) return rc;
+    return fp4_by_type(dtype, [&](auto dt) {
+        return fp4_by_format(format, [&](auto fm) {
+            using T = typename Fp4Type<decltype(dt)::value>::T;
+            return launched(launch_pdl(fp4_dequant_kernel<decltype(dt)::value, decltype(fm)::value>,
+                                       dim3((unsigned)fp4_patches(rows, K)), dim3(kThreads), (size_t)0,
+                                       static_cast<cudaStream_t>(stream), codes, scales, rows, K, g,
+                                       static_cast<T *>(y), ldy));
+        });
+    });
+}
+
+static int fp4_zero(DeviceInfo *dev, void *y, int dtype, int64_t M, int64_t N, int64_t ldy, cudaStream_t st) {
+    const int grid = grid_for(M * N, kThreads * 4, dev->sm_count);
+    if (dtype == BITNET_FP16)
+        fp4_zero_kernel<<<grid, kThreads, 0, st>>>(static_cast<__half *>(y), M, N, ldy);
+    else
+        fp4_zero_kernel<<<grid, kThreads, 0, st>>>(static_cast<__nv_bfloat16 *>(y), M, N, ldy);
+    return launched();
+}
+
+BITNET_API int bitnet_fp4_gemm(const uint8_t *a, const uint8_t *a_scales, const float *ga, const uint8_t *w,
+                               const uint8_t *w_scales, const float *gw, int format, void *y, int dtype, int64_t M,
+                               int64_t N, int64_t K, int64_t ldy, void *workspace, int64_t workspace_bytes,
+                               void *stream) {
+    (void)workspace, (void)workspace_bytes;
+    if (!sizes_ok(M, 1, K) || !sizes_ok(N, 1, K) || !fp4_format_ok(format) ||
+        (dtype != BITNET_BF16 && dtype != BITNET_FP16) || !fp4_ld_ok(M, N, ldy))
+        return BITNET_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return BITNET_OK;
+    if (y == nullptr || (K > 0 && (a == nullptr || a_scales == nullptr || w == nullptr || w_scales == nullptr)))
+        return BITNET_ERR_INVALID_ARG;
+    if (!aligned(a, 16) || !aligned(a_scales, 16) || !aligned(w, 16) || !aligned(w_scales, 16) || !aligned(y, 2) ||
+        !aligned(ga, 4) || !aligned(gw, 4))
+        return BITNET_ERR_ALIGNMENT;
+    DeviceInfo *dev = nullptr;
+    const int rc = device_info(&dev);
+    if (rc != BITNET_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (K == 0) return fp4_zero(dev, y, dtype, M, N, ldy, st);
+    return launch_fp4_gemm(dev, a, a_scales, ga, w, w_scales, gw, format, y, dtype, M, N, K, ldy, st);
+}
+
+BITNET_API int bitnet_fp4_linear(const void *x, int xdtype, int64_t ldx, const float *ga, const uint8_t *w,
+                                 const uint8_t *w_scales, const float *gw, int format, void *y, int ydtype, int64_t M,
+                                 int64_t N, int64_t K, int64_t ldy, void *workspace, int64_t workspace_bytes,
+                                 void *stream) {
+    if (!sizes_ok(M, 1, K) || !sizes_ok(N, 1, K) || !fp4_format_ok(format) || !fp4_dtype_ok(xdtype) ||
+        (ydtype != BITNET_BF16 && ydtype != BITNET_FP16) || !fp4_ld_ok(M, N, ldy) || !fp4_ld_ok(M, K, ldx))
+        return BITNET_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return BITNET_OK;
+    if (y == nullptr || (K > 0 && (x == nullptr || w == nullptr || w_scales == nullptr))) return BITNET_ERR_INVALID_ARG;
+    if (!aligned(x, fp4_dtype_size(xdtype)) || !aligned(w, 16) || !aligned(w_scales, 16) || !aligned(y, 2) ||
+        !aligned(ga, 4) || !aligned(gw, 4))
+        return BITNET_ERR_ALIGNMENT;
+    const int64_t cb = round_up(bitnet_fp4_code_bytes(M, K), 256);
+    const int64_t need = K > 0 ? cb + bitnet_fp4_scale_bytes(M, K, format) : 0;
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return BITNET_ERR_WORKSPACE;
+    if (need > 0 && !aligned(workspace, 256)) return BITNET_ERR_ALIGNMENT;
+    if (fp4_patches(M, K) > (1LL << 31) - 1) return BITNET_ERR_UNSUPPORTED;
+    DeviceInfo *dev = nullptr;
+    int rc = device_info(&dev);
+    if (rc != BITNET_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (K == 0) return fp4_zero(dev, y, ydtype, M, N, ldy, st);
+    uint8_t *codes = static_cast<uint8_t *>(workspace), *scales = codes + cb;
+    if ((rc = launch_fp4_quant(x, xdtype, M, K, ldx, format, ga, codes, scales, st)) != BITNET_OK) return rc;
+    return launch_fp4_gemm(dev, codes, scales, ga, w, w_scales, gw, format, y, ydtype, M, N, K, ldy, st);
 }
 
 BITNET_API int bitnet_get_device_error(void *stream) {
