@@ -226,10 +226,9 @@ BITNET_API int64_t bitnet_fp4_code_bytes(int64_t rows, int64_t K);
 BITNET_API int64_t bitnet_fp4_scale_bytes(int64_t rows, int64_t K, int format);
 
 /*
- * Workspace bytes that bitnet_fp4_tensor_scale (M = its rows), bitnet_fp4_gemm
- * and bitnet_fp4_linear need for an M x N x K problem (the maximum over the
- * three), or -1 for invalid sizes or an unknown format.  Depends only on its
- * arguments.
+ * Workspace bytes that bitnet_fp4_tensor_scale (M = its rows, any N) and
+ * bitnet_fp4_linear need for an M x N x K problem (the larger of the two), or
+ * -1 for invalid sizes or an unknown format.  Depends only on its arguments.
  */
 BITNET_API int64_t bitnet_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K, int format);
 
@@ -278,17 +277,19 @@ BITNET_API int bitnet_fp4_dequant(const uint8_t *codes, const uint8_t *scales, i
  *   ga, gw       device, 1 float each, or NULL
  *   y            device, dtype BITNET_BF16 or BITNET_FP16 [M, N], row stride
  *                ldy >= N elements (output)
- *   workspace    device, >= bitnet_fp4_workspace_bytes(M, N, K, format) bytes,
- *                256-byte aligned
  */
 BITNET_API int bitnet_fp4_gemm(const uint8_t *a, const uint8_t *a_scales, const float *ga, const uint8_t *w,
                                const uint8_t *w_scales, const float *gw, int format, void *y, int dtype, int64_t M,
-                               int64_t N, int64_t K, int64_t ldy, void *workspace, int64_t workspace_bytes,
-                               void *stream);
+                               int64_t N, int64_t K, int64_t ldy, void *stream);
 
 /*
  * Linear layer: quantises x with the tensor scale ga, then the product above;
- * the values are those of bitnet_fp4_quant followed by bitnet_fp4_gemm.
+ * the values are those of bitnet_fp4_quant followed by bitnet_fp4_gemm.  Up to
+ * 16 tokens are quantised inside the product's launch and need no workspace
+ * (it may be NULL); more are quantised into it first.
+ *   x, ldx       as in bitnet_fp4_quant; the rest as in bitnet_fp4_gemm
+ *   workspace    device, >= bitnet_fp4_workspace_bytes(M, N, K, format) bytes,
+ *                256-byte aligned
  */
 BITNET_API int bitnet_fp4_linear(const void *x, int xdtype, int64_t ldx, const float *ga, const uint8_t *w,
                                  const uint8_t *w_scales, const float *gw, int format, void *y, int ydtype, int64_t M,

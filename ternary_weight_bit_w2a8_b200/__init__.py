@@ -52,7 +52,7 @@ _SIGNATURES = {
     "bitnet_fp4_tensor_scale": (ctypes.c_int, [_p, _int, _i64, _i64, _i64, _p, _p, _i64, _p]),
     "bitnet_fp4_quant": (ctypes.c_int, [_p, _int, _i64, _i64, _i64, _int, _p, _p, _p, _p]),
     "bitnet_fp4_dequant": (ctypes.c_int, [_p, _p, _i64, _i64, _int, _p, _p, _int, _i64, _p]),
-    "bitnet_fp4_gemm": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _int, _p, _int, _i64, _i64, _i64, _i64, _p, _i64, _p]),
+    "bitnet_fp4_gemm": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _int, _p, _int, _i64, _i64, _i64, _i64, _p]),
     "bitnet_fp4_linear": (ctypes.c_int, [_p, _int, _i64, _p, _p, _p, _p, _int, _p, _int, _i64, _i64, _i64, _i64, _p,
                                          _i64, _p]),
     "bitnet_get_device_error": (ctypes.c_int, [_p]),
@@ -237,61 +237,36 @@ def bitnet_w2a8_gemm_noalloc(q, packed, N: int, y=None, stream=None):
 
 
 # ------------------------------------------------------------------ 4-bit floating point
-# The matrices here may lie on any one CUDA device (it is made current for the
-# call); x and y may be row-strided views, everything else is contiguous.
+# The tensors of a call lie on one CUDA device, which need not be the current
+# one; x and y may be row-strided views, everything else is contiguous.  These
+# calls are short (a decode step is a few microseconds on the GPU), so the
+# checks avoid what costs the interpreter most: device objects, context
+# managers and size queries through ctypes.
 
-def _fp4_dtype(t, name="x"):
+_torch = None
+_dtypes = {}
+
+
+def _load_torch():
+    global _torch
     import torch
-    d = {torch.bfloat16: BITNET_BF16, torch.float16: BITNET_FP16, torch.float32: BITNET_FP32}.get(t)
-    if d is None:
-        raise ValueError(f"{name} must be bfloat16, float16 or float32")
-    return d
-
-
-def _rows(t, name, device=None):
-    """(rows, columns, row stride) of a 2-D CUDA tensor whose rows are contiguous."""
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{name} must be a CUDA tensor on the call's device")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be 2-D with contiguous rows")
-    rows, cols = t.shape
-    return rows, cols, (t.stride(0) if rows > 1 else cols)
-
-
-def _plain(t, name, dtype, device, numel):
-    if t is None:
-        return
-    if not t.is_cuda or t.device != device or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor on the call's device")
-    if t.numel() < numel:
-        raise ValueError(f"{name} holds {t.numel()} elements, {numel} are needed")
-
-
-def _fp4_matrix(codes, scales, K, fmt, device, name):
-    """Rows of a quantised matrix whose codes are [rows, K_pad / 2]."""
-    import torch
-    if codes.dim() != 2 or codes.shape[1] != bitnet_fp4_code_bytes(1, K):
-        raise ValueError(f"{name} must be [rows, {bitnet_fp4_code_bytes(1, K)}] for K = {K}")
-    rows = codes.shape[0]
-    _plain(codes, name, torch.uint8, device, 0)
-    _plain(scales, f"{name}'s scales", torch.uint8, device, bitnet_fp4_scale_bytes(rows, K, fmt))
-    return rows
+    _torch = torch
+    _dtypes.update({torch.bfloat16: BITNET_BF16, torch.float16: BITNET_FP16, torch.float32: BITNET_FP32})
+    return torch
 
 
 class _on:
-    """Makes `device` and, where given, `stream` current: what the call
+    """Makes device `index` and, where given, `stream` current: what a call
     allocates belongs to the stream that it runs on."""
 
-    def __init__(self, device, stream):
-        import torch
-        self.device = torch.cuda.device(device)
-        self.stream = torch.cuda.stream(stream) if stream is not None else None
+    def __init__(self, index, stream):
+        self.device = _torch.cuda.device(index)
+        self.stream = None if stream is None else _torch.cuda.stream(stream)
 
     def __enter__(self):
         self.device.__enter__()
         if self.stream is not None:
             self.stream.__enter__()
-        return _stream()
 
     def __exit__(self, *exc):
         if self.stream is not None:
@@ -299,12 +274,59 @@ class _on:
         self.device.__exit__(*exc)
 
 
-def _fp4_workspace(ws, need, device):
-    import torch
-    if ws is None:
-        return torch.empty(max(256, need), dtype=torch.uint8, device=device)
-    _plain(ws, "ws", torch.uint8, device, 0)
-    return ws
+def _device_of(t, name):
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return index
+
+
+def _elsewhere(index, stream):
+    """Whether a call on device `index` needs _on: another device or stream than the current ones."""
+    return stream is not None or index != _torch._C._cuda_getDevice()
+
+
+def _float_type(t, name):
+    d = _dtypes.get(t)
+    if d is None:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, not {t}")
+    return d
+
+
+def _rows(t, name, index, shape=None):
+    """Row stride of a 2-D tensor whose rows are contiguous."""
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on the call's CUDA device")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with contiguous rows")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _flat(t, name, dtype, index, numel):
+    """Pointer of a contiguous tensor of at least `numel` elements (None for None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on the call's CUDA device")
+    if t.numel() < numel:
+        raise ValueError(f"{name} holds {t.numel()} elements, {numel} are needed")
+    return t.data_ptr()
+
+
+def _scale_bytes(rows, K, fmt):
+    if fmt != BITNET_FP4_MX and fmt != BITNET_FP4_NV:
+        raise ValueError("fmt must be BITNET_FP4_MX or BITNET_FP4_NV")
+    return -(-rows // 128) * -(-K // 128) * (512 if fmt == BITNET_FP4_MX else 1024)
+
+
+def _matrix(codes, scales, K, fmt, index, name):
+    """Pointers of a quantised matrix [rows, K]."""
+    if codes.dim() != 2 or codes.shape[1] != -(-K // 128) * 64:
+        raise ValueError(f"{name} must be [rows, {-(-K // 128) * 64}] for K = {K}, not {list(codes.shape)}")
+    return (_flat(codes, name, _torch.uint8, index, 0),
+            _flat(scales, f"{name}'s scales", _torch.uint8, index, _scale_bytes(codes.shape[0], K, fmt)))
 
 
 def bitnet_fp4_code_bytes(rows: int, K: int) -> int:
@@ -328,93 +350,114 @@ def bitnet_fp4_workspace_bytes(M: int, N: int, K: int, fmt: int) -> int:
     return n
 
 
+def _fp4_workspace(ws, M, N, K, fmt, t, index):
+    """The caller's workspace, or one of the size needed on t's device (none where none is needed)."""
+    if ws is None:
+        need = bitnet_fp4_workspace_bytes(M, N, K, fmt)
+        return t.new_empty(need, dtype=_torch.uint8) if need else None
+    _flat(ws, "ws", _torch.uint8, index, 0)
+    return ws
+
+
 def bitnet_fp4_tensor_scale(x, g=None, ws=None, stream=None):
     """Tensor scale of the NV format, max|x| / 2688 over the finite values of x -> float32 tensor [1]."""
-    import torch
-    rows, K, ldx = _rows(x, "x")
-    with _on(x.device, stream) as st:
-        if g is None:
-            g = torch.empty(1, dtype=torch.float32, device=x.device)
-        _plain(g, "g", torch.float32, x.device, 1)
-        ws = _fp4_workspace(ws, bitnet_fp4_workspace_bytes(rows, 1, K, BITNET_FP4_NV) if ws is None else 0, x.device)
-        _check(lib().bitnet_fp4_tensor_scale(_ptr(x), _fp4_dtype(x.dtype), rows, K, ldx, _ptr(g), _ptr(ws), ws.numel(),
-                                             st), "bitnet_fp4_tensor_scale")
+    torch = _torch or _load_torch()
+    index = _device_of(x, "x")
+    if _elsewhere(index, stream):
+        with _on(index, stream):
+            return bitnet_fp4_tensor_scale(x, g, ws)
+    ldx = _rows(x, "x", index)
+    rows, K = x.shape
+    if g is None:
+        g = x.new_empty(1, dtype=torch.float32)
+    ws = _fp4_workspace(ws, rows, 1, K, BITNET_FP4_NV, x, index)
+    _check(lib().bitnet_fp4_tensor_scale(x.data_ptr(), _float_type(x.dtype, "x"), rows, K, ldx,
+                                         _flat(g, "g", torch.float32, index, 1), ws.data_ptr(), ws.numel(),
+                                         torch._C._cuda_getCurrentRawStream(index)), "bitnet_fp4_tensor_scale")
     return g
 
 
 def bitnet_fp4_quant(x, fmt: int, g=None, codes=None, scales=None, stream=None):
     """Quantises x [rows, K] -> (codes uint8 [rows, K_pad / 2], scales uint8 [bitnet_fp4_scale_bytes(rows, K, fmt)])."""
-    import torch
-    rows, K, ldx = _rows(x, "x")
-    with _on(x.device, stream) as st:
-        if codes is None:
-            codes = torch.empty((rows, bitnet_fp4_code_bytes(1, K)), dtype=torch.uint8, device=x.device)
-        if scales is None:
-            scales = torch.empty(bitnet_fp4_scale_bytes(rows, K, fmt), dtype=torch.uint8, device=x.device)
-        if _fp4_matrix(codes, scales, K, fmt, x.device, "codes") != rows:
-            raise ValueError("codes and x differ in their rows")
-        _plain(g, "g", torch.float32, x.device, 1)
-        _check(lib().bitnet_fp4_quant(_ptr(x), _fp4_dtype(x.dtype), rows, K, ldx, fmt, _ptr(g), _ptr(codes),
-                                      _ptr(scales), st), "bitnet_fp4_quant")
+    torch = _torch or _load_torch()
+    index = _device_of(x, "x")
+    if _elsewhere(index, stream):
+        with _on(index, stream):
+            return bitnet_fp4_quant(x, fmt, g, codes, scales)
+    ldx = _rows(x, "x", index)
+    rows, K = x.shape
+    if codes is None:
+        codes = x.new_empty((rows, -(-K // 128) * 64), dtype=torch.uint8)
+    if scales is None:
+        scales = x.new_empty(_scale_bytes(rows, K, fmt), dtype=torch.uint8)
+    cp, sp = _matrix(codes, scales, K, fmt, index, "codes")
+    if codes.shape[0] != rows:
+        raise ValueError("codes and x differ in their rows")
+    _check(lib().bitnet_fp4_quant(x.data_ptr(), _float_type(x.dtype, "x"), rows, K, ldx, fmt,
+                                  _flat(g, "g", torch.float32, index, 1), cp, sp,
+                                  torch._C._cuda_getCurrentRawStream(index)), "bitnet_fp4_quant")
     return codes, scales
 
 
 def bitnet_fp4_dequant(codes, scales, K: int, fmt: int, g=None, dtype=None, y=None, stream=None):
     """The values of a quantised matrix -> y [rows, K] (bfloat16 unless dtype or y says otherwise)."""
-    import torch
-    rows = _fp4_matrix(codes, scales, K, fmt, codes.device, "codes")
-    with _on(codes.device, stream) as st:
-        if y is None:
-            y = torch.empty((rows, K), dtype=dtype or torch.bfloat16, device=codes.device)
-        yr, yk, ldy = _rows(y, "y", codes.device)
-        if (yr, yk) != (rows, K):
-            raise ValueError(f"y must be [{rows}, {K}]")
-        _plain(g, "g", torch.float32, codes.device, 1)
-        _check(lib().bitnet_fp4_dequant(_ptr(codes), _ptr(scales), rows, K, fmt, _ptr(g), _ptr(y),
-                                        _fp4_dtype(y.dtype, "y"), ldy, st), "bitnet_fp4_dequant")
+    torch = _torch or _load_torch()
+    index = _device_of(codes, "codes")
+    if _elsewhere(index, stream):
+        with _on(index, stream):
+            return bitnet_fp4_dequant(codes, scales, K, fmt, g, dtype, y)
+    cp, sp = _matrix(codes, scales, K, fmt, index, "codes")
+    rows = codes.shape[0]
+    if y is None:
+        y = codes.new_empty((rows, K), dtype=dtype or torch.bfloat16)
+    ldy = _rows(y, "y", index, (rows, K))
+    _check(lib().bitnet_fp4_dequant(cp, sp, rows, K, fmt, _flat(g, "g", torch.float32, index, 1), y.data_ptr(),
+                                    _float_type(y.dtype, "y"), ldy, torch._C._cuda_getCurrentRawStream(index)),
+           "bitnet_fp4_dequant")
     return y
 
 
-def bitnet_fp4_gemm(a, a_scales, w, w_scales, K: int, fmt: int, ga=None, gw=None, dtype=None, y=None, ws=None,
-                    stream=None):
+def bitnet_fp4_gemm(a, a_scales, w, w_scales, K: int, fmt: int, ga=None, gw=None, dtype=None, y=None, stream=None):
     """y = A W^T of quantised A [M, K] and W [N, K] -> [M, N] (bfloat16 or float16)."""
-    import torch
-    dev = a.device
-    M = _fp4_matrix(a, a_scales, K, fmt, dev, "a")
-    N = _fp4_matrix(w, w_scales, K, fmt, dev, "w")
-    with _on(dev, stream) as st:
-        if y is None:
-            y = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=dev)
-        ym, yn, ldy = _rows(y, "y", dev)
-        if (ym, yn) != (M, N):
-            raise ValueError(f"y must be [{M}, {N}]")
-        _plain(ga, "ga", torch.float32, dev, 1)
-        _plain(gw, "gw", torch.float32, dev, 1)
-        ws = _fp4_workspace(ws, bitnet_fp4_workspace_bytes(M, N, K, fmt) if ws is None else 0, dev)
-        _check(lib().bitnet_fp4_gemm(_ptr(a), _ptr(a_scales), _ptr(ga), _ptr(w), _ptr(w_scales), _ptr(gw), fmt,
-                                     _ptr(y), _fp4_dtype(y.dtype, "y"), M, N, K, ldy, _ptr(ws), ws.numel(), st),
-               "bitnet_fp4_gemm")
+    torch = _torch or _load_torch()
+    index = _device_of(a, "a")
+    if _elsewhere(index, stream):
+        with _on(index, stream):
+            return bitnet_fp4_gemm(a, a_scales, w, w_scales, K, fmt, ga, gw, dtype, y)
+    ap, asp = _matrix(a, a_scales, K, fmt, index, "a")
+    wp, wsp = _matrix(w, w_scales, K, fmt, index, "w")
+    M, N = a.shape[0], w.shape[0]
+    if y is None:
+        y = a.new_empty((M, N), dtype=dtype or torch.bfloat16)
+    ldy = _rows(y, "y", index, (M, N))
+    _check(lib().bitnet_fp4_gemm(ap, asp, _flat(ga, "ga", torch.float32, index, 1), wp, wsp,
+                                 _flat(gw, "gw", torch.float32, index, 1), fmt, y.data_ptr(),
+                                 _float_type(y.dtype, "y"), M, N, K, ldy,
+                                 torch._C._cuda_getCurrentRawStream(index)), "bitnet_fp4_gemm")
     return y
 
 
 def bitnet_fp4_linear(x, w, w_scales, fmt: int, ga=None, gw=None, dtype=None, y=None, ws=None, stream=None):
     """y = quantised(x) W^T: x [M, K] of any type, quantised W [N, K] -> [M, N] (bfloat16 or float16)."""
-    import torch
-    dev = x.device
-    M, K, ldx = _rows(x, "x")
-    N = _fp4_matrix(w, w_scales, K, fmt, dev, "w")
-    with _on(dev, stream) as st:
-        if y is None:
-            y = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=dev)
-        ym, yn, ldy = _rows(y, "y", dev)
-        if (ym, yn) != (M, N):
-            raise ValueError(f"y must be [{M}, {N}]")
-        _plain(ga, "ga", torch.float32, dev, 1)
-        _plain(gw, "gw", torch.float32, dev, 1)
-        ws = _fp4_workspace(ws, bitnet_fp4_workspace_bytes(M, N, K, fmt) if ws is None else 0, dev)
-        _check(lib().bitnet_fp4_linear(_ptr(x), _fp4_dtype(x.dtype), ldx, _ptr(ga), _ptr(w), _ptr(w_scales), _ptr(gw),
-                                       fmt, _ptr(y), _fp4_dtype(y.dtype, "y"), M, N, K, ldy, _ptr(ws), ws.numel(), st),
-               "bitnet_fp4_linear")
+    torch = _torch or _load_torch()
+    index = _device_of(x, "x")
+    if _elsewhere(index, stream):
+        with _on(index, stream):
+            return bitnet_fp4_linear(x, w, w_scales, fmt, ga, gw, dtype, y, ws)
+    ldx = _rows(x, "x", index)
+    M, K = x.shape
+    wp, wsp = _matrix(w, w_scales, K, fmt, index, "w")
+    N = w.shape[0]
+    if y is None:
+        y = x.new_empty((M, N), dtype=dtype or torch.bfloat16)
+    ldy = _rows(y, "y", index, (M, N))
+    if ws is not None or M > 16:  # fewer tokens need none
+        ws = _fp4_workspace(ws, M, N, K, fmt, x, index)
+    _check(lib().bitnet_fp4_linear(x.data_ptr(), _float_type(x.dtype, "x"), ldx,
+                                   _flat(ga, "ga", torch.float32, index, 1), wp, wsp,
+                                   _flat(gw, "gw", torch.float32, index, 1), fmt, y.data_ptr(),
+                                   _float_type(y.dtype, "y"), M, N, K, ldy, _ptr(ws), 0 if ws is None else ws.numel(),
+                                   torch._C._cuda_getCurrentRawStream(index)), "bitnet_fp4_linear")
     return y
 
 

@@ -13,6 +13,7 @@
 #include "common.cuh"
 #include "fp4.cuh"
 #include "fp4_gemm.cuh"
+#include "fp4_gemm_pair.cuh"
 #include "gemv.cuh"
 #include "gemv_tma.cuh"
 #include "gemm_tc.cuh"
@@ -961,57 +962,174 @@ int launch_fp4_quant(const void *x, int dtype, int64_t rows, int64_t K, int64_t 
     });
 }
 
-template <int FMT, int BT, int DT>
-int launch_fp4_gemm_variant(DeviceInfo *dev, const CUtensorMap &pmap, const CUtensorMap &qmap, const Fp4GemmArgs &a,
-                            cudaStream_t st) {
-    (void)dev;
-    auto kern = fp4_gemm_kernel<FMT, BT, DT>;
-    constexpr size_t smem = Fp4Smem<FMT, BT>::kBytes + 1024;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+// Raises a kernel's shared-memory limit once per device.
+template <typename Kern>
+bool fp4_opt_in(DeviceInfo *dev, Kern kern, size_t smem, std::atomic<uint64_t> &set) {
+    const uint64_t bit = 1ull << (dev - g_dev);
+    if (set.load(std::memory_order_acquire) & bit) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
+    set.fetch_or(bit, std::memory_order_release);
+    return true;
+}
+
+template <typename Kern, typename... Args>
+cudaError_t launch_pdl_cluster(Kern kern, unsigned grid, unsigned block, unsigned cluster, size_t smem, cudaStream_t st,
+                               Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 0 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+bool fp4_code_map(CUtensorMap *m, const uint8_t *codes, int64_t rows, int64_t K, int box) {
+    const uint64_t rb = (uint64_t)fp4_row_bytes(K);
+    return encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, rb, (uint64_t)rows, rb, 128, (uint32_t)box,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
+// Tokens that the small kernel takes; more go to the pair kernel.
+constexpr int kFp4SmallTokens = 128;
+
+// CTAs per weight tile of the small kernel: the split whose waves of CTAs (two
+// per SM) take the fewest stages, a CTA's start and end counted as two.  From
+// the sizes alone, so that the sums' grouping depends on nothing else.
+int fp4_split(int64_t N, int64_t K) {
+    const int64_t tiles = ceil_div(N, kFp4Rows), nk = ceil_div(k_pad(K), kFp4StageK);
+    int best = 1;
+    int64_t cost = INT64_MAX;
+    for (int s = 1; s <= kFp4MaxSplit && s <= nk; s *= 2) {
+        const int64_t c = ceil_div(tiles * s, 2 * 148) * (ceil_div(nk, s) + 2);
+        if (c < cost) cost = c, best = s;
+    }
+    return best;
+}
+
+template <int FMT, int BT, bool QX>
+int launch_fp4_small_variant(DeviceInfo *dev, const CUtensorMap &wmap, const CUtensorMap &amap, const Fp4SmallArgs &a,
+                             cudaStream_t st) {
+    auto kern = fp4_small_kernel<FMT, BT, QX>;
+    constexpr size_t smem = Fp4Small<FMT, BT>::kBytes + 1024;
+    static std::atomic<uint64_t> set{0};
+    if (!fp4_opt_in(dev, kern, smem, set)) return BITNET_ERR_CUDA;
+    const int64_t grid = ceil_div(a.N, kFp4Rows) * a.split;
+    if (grid > (int64_t)1 << 30) return BITNET_ERR_UNSUPPORTED;
+    return launched(launch_pdl_cluster(kern, (unsigned)grid, kFp4Threads, (unsigned)a.split, smem, st, wmap, amap, a));
+}
+
+// codes == null: the tokens are quantised in the kernel (a.x).
+int launch_fp4_small(DeviceInfo *dev, const uint8_t *codes, const uint8_t *w, int format, Fp4SmallArgs a,
+                     cudaStream_t st) {
+    a.split = fp4_split(a.N, a.K);
+    const int BT = a.M <= 16 ? 16 : (a.M <= 32 ? 32 : (a.M <= 64 ? 64 : 128));
+    CUtensorMap wmap, amap;
+    memset(&amap, 0, sizeof(amap));
+    if (!fp4_code_map(&wmap, w, a.N, a.K, kFp4Rows) || (codes != nullptr && !fp4_code_map(&amap, codes, a.M, a.K, BT)))
         return BITNET_ERR_CUDA;
-    const int64_t units = (int64_t)a.tiles_p * ceil_div(a.Q, BT);
-    if (units > (int64_t)1 << 30) return BITNET_ERR_UNSUPPORTED;
-    return launched(launch_pdl(kern, dim3((unsigned)units), dim3(kFp4Threads), smem, st, pmap, qmap, a));
+    return fp4_by_format(format, [&](auto fm) {
+        constexpr int F = decltype(fm)::value;
+        if (codes == nullptr) return launch_fp4_small_variant<F, kFp4FusedTokens, true>(dev, wmap, amap, a, st);
+        switch (BT) {
+            case 16: return launch_fp4_small_variant<F, 16, false>(dev, wmap, amap, a, st);
+            case 32: return launch_fp4_small_variant<F, 32, false>(dev, wmap, amap, a, st);
+            case 64: return launch_fp4_small_variant<F, 64, false>(dev, wmap, amap, a, st);
+            default: return launch_fp4_small_variant<F, 128, false>(dev, wmap, amap, a, st);
+        }
+    });
+}
+
+// Weight rows per tile of the pair kernel: the width whose rounds over the 74
+// pairs take the fewest cycles, a 256-k stage counted at what an SM loads for
+// it (64 bytes a cycle) and a tile's start and end with the rest.
+int fp4_pair_width(int64_t M, int64_t N, int64_t K) {
+    const int64_t nk = ceil_div(k_pad(K), kFp4StageK), tm = ceil_div(M, 256);
+    int best = 256;
+    int64_t cost = INT64_MAX;
+    for (int bt = 256; bt >= 64; bt /= 2) {
+        const int64_t stage = bt == 256 ? 608 : (bt == 128 ? 448 : 384), end = bt == 256 ? 800 : 200;
+        const int64_t c = ceil_div(tm * ceil_div(N, bt), 74) * (nk * stage + end);
+        if (c < cost) cost = c, best = bt;
+    }
+    return best;
+}
+
+template <int FMT, int BT>
+int launch_fp4_pair_variant(DeviceInfo *dev, const CUtensorMap &amap, const CUtensorMap &wmap, const CUtensorMap &samap,
+                            const CUtensorMap &swmap, const Fp4PairArgs &a, cudaStream_t st) {
+    auto kern = fp4_pair_kernel<FMT, BT>;
+    constexpr size_t smem = Fp4Pair<FMT, BT>::kBytes + 1024;
+    static std::atomic<uint64_t> set{0};
+    if (!fp4_opt_in(dev, kern, smem, set)) return BITNET_ERR_CUDA;
+    const int64_t units = (int64_t)a.tiles_m * a.tiles_n, pairs = dev->sm_count / 2;
+    return launched(launch_pdl_cluster(kern, (unsigned)(2 * (units < pairs ? units : pairs)), kFp4PairThreads, 0, smem, st,
+                                       amap, wmap, samap, swmap, a));
+}
+
+int launch_fp4_pair(DeviceInfo *dev, const uint8_t *codes, const uint8_t *sa, const float *ga, const uint8_t *w,
+                    const uint8_t *sw, const float *gw, int format, void *y, int dtype, int64_t M, int64_t N, int64_t K,
+                    int64_t ldy, cudaStream_t st) {
+    const int BT = fp4_pair_width(M, N, K);
+    if (ceil_div(M, 256) * ceil_div(N, BT) > (int64_t)1 << 30) return BITNET_ERR_UNSUPPORTED;
+    const int64_t tiles = fp4_scale_tiles(K, format);
+    if ((ceil_div(M, 128) + 1) * tiles > INT32_MAX || (ceil_div(N, 128) + 1) * tiles > INT32_MAX || N > INT32_MAX)
+        return BITNET_ERR_UNSUPPORTED;  // TMA coordinates
+    CUtensorMap amap, wmap, samap, swmap;
+    auto scale_map = [&](CUtensorMap *m, const uint8_t *s, int64_t rows) {
+        return encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_INT32, s, kFp4TileBytes / 4, (uint64_t)(ceil_div(rows, 128) * tiles),
+                         kFp4TileBytes, kFp4TileBytes / 4, format == BITNET_FP4_MX ? 2 : 4, CU_TENSOR_MAP_SWIZZLE_NONE,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    };
+    if (!fp4_code_map(&amap, codes, M, K, 128) || !fp4_code_map(&wmap, w, N, K, BT / 2) || !scale_map(&samap, sa, M) ||
+        !scale_map(&swmap, sw, N))
+        return BITNET_ERR_CUDA;
+    Fp4PairArgs a{};
+    a.M = M, a.N = N, a.K = K, a.ldy = ldy;
+    a.ga = ga, a.gw = gw;
+    a.y = y;
+    a.ytype = dtype;
+    a.tiles_m = (int)ceil_div(M, 256);
+    a.tiles_n = (int)ceil_div(N, BT);
+    a.vec = aligned(y, 32) && ldy % 16 == 0;
+    return fp4_by_format(format, [&](auto fm) {
+        constexpr int F = decltype(fm)::value;
+        switch (BT) {
+            case 64: return launch_fp4_pair_variant<F, 64>(dev, amap, wmap, samap, swmap, a, st);
+            case 128: return launch_fp4_pair_variant<F, 128>(dev, amap, wmap, samap, swmap, a, st);
+            default: return launch_fp4_pair_variant<F, 256>(dev, amap, wmap, samap, swmap, a, st);
+        }
+    });
+}
+
+Fp4SmallArgs fp4_small_args(const uint8_t *sw, const float *ga, const float *gw, void *y, int dtype, int64_t M,
+                            int64_t N, int64_t K, int64_t ldy) {
+    Fp4SmallArgs a{};
+    a.sw = sw;
+    a.ytype = dtype;
+    a.M = (int)M;
+    a.N = N, a.K = K, a.ldy = ldy;
+    a.ga = ga, a.gw = gw;
+    a.y = y;
+    return a;
 }
 
 int launch_fp4_gemm(DeviceInfo *dev, const uint8_t *a, const uint8_t *sa, const float *ga, const uint8_t *w,
                     const uint8_t *sw, const float *gw, int format, void *y, int dtype, int64_t M, int64_t N, int64_t K,
                     int64_t ldy, cudaStream_t st) {
-    if (tensor_map_encoder() == nullptr) return BITNET_ERR_CUDA;
-    // few tokens: the weights are the P operand and the tokens one tile of Q
-    const bool tokens_q = M <= 128;
-    const int BT = M <= 16 ? 16 : (M <= 64 ? 64 : 128);
-    Fp4GemmArgs g{};
-    const uint8_t *p = tokens_q ? w : a, *q = tokens_q ? a : w;
-    g.sp = tokens_q ? sw : sa;
-    g.sq = tokens_q ? sa : sw;
-    g.P = tokens_q ? N : M;
-    g.Q = tokens_q ? M : N;
-    g.K = K;
-    g.stride_p = tokens_q ? 1 : ldy;
-    g.stride_q = tokens_q ? ldy : 1;
-    g.ga = ga;
-    g.gw = gw;
-    g.y = y;
-    g.tiles_p = (int)ceil_div(g.P, kFp4Rows);
-    const uint64_t rb = (uint64_t)fp4_row_bytes(K);
-    CUtensorMap pmap, qmap;
-    if (!encode_2d(&pmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, rb, (uint64_t)g.P, rb, 128, kFp4Rows,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
-        !encode_2d(&qmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, rb, (uint64_t)g.Q, rb, 128, (uint32_t)BT,
-                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B))
-        return BITNET_ERR_CUDA;
-    return fp4_by_format(format, [&](auto fm) {
-        constexpr int F = decltype(fm)::value;
-        auto by_bt = [&](auto bt) {
-            constexpr int B = decltype(bt)::value;
-            if (dtype == BITNET_FP16) return launch_fp4_gemm_variant<F, B, BITNET_FP16>(dev, pmap, qmap, g, st);
-            return launch_fp4_gemm_variant<F, B, BITNET_BF16>(dev, pmap, qmap, g, st);
-        };
-        if (BT == 16) return by_bt(std::integral_constant<int, 16>{});
-        if (BT == 64) return by_bt(std::integral_constant<int, 64>{});
-        return by_bt(std::integral_constant<int, 128>{});
-    });
+    if (M > kFp4SmallTokens)
+        return launch_fp4_pair(dev, a, sa, ga, w, sw, gw, format, y, dtype, M, N, K, ldy, st);
+    Fp4SmallArgs s = fp4_small_args(sw, ga, gw, y, dtype, M, N, K, ldy);
+    s.sa = sa;
+    return launch_fp4_small(dev, a, w, format, s, st);
 }
 
 // y = 0 (K == 0).
@@ -1232,7 +1350,8 @@ BITNET_API int64_t bitnet_fp4_scale_bytes(int64_t rows, int64_t K, int format) {
 BITNET_API int64_t bitnet_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K, int format) {
     if (!sizes_ok(M, 1, K) || !sizes_ok(N, 1, K) || !fp4_format_ok(format)) return -1;
     const int64_t scale = (int64_t)kFp4ScaleMaxBlocks * 4;
-    const int64_t linear = round_up(bitnet_fp4_code_bytes(M, K), 256) + round_up(bitnet_fp4_scale_bytes(M, K, format), 256);
+    const int64_t linear =
+        M > kFp4FusedTokens && N > 0 ? round_up(M * fp4_row_bytes(K), 256) + bitnet_fp4_scale_bytes(M, K, format) : 0;
     return linear > scale ? linear : scale;
 }
 
@@ -1312,9 +1431,7 @@ static int fp4_zero(DeviceInfo *dev, void *y, int dtype, int64_t M, int64_t N, i
 
 BITNET_API int bitnet_fp4_gemm(const uint8_t *a, const uint8_t *a_scales, const float *ga, const uint8_t *w,
                                const uint8_t *w_scales, const float *gw, int format, void *y, int dtype, int64_t M,
-                               int64_t N, int64_t K, int64_t ldy, void *workspace, int64_t workspace_bytes,
-                               void *stream) {
-    (void)workspace, (void)workspace_bytes;
+                               int64_t N, int64_t K, int64_t ldy, void *stream) {
     if (!sizes_ok(M, 1, K) || !sizes_ok(N, 1, K) || !fp4_format_ok(format) ||
         (dtype != BITNET_BF16 && dtype != BITNET_FP16) || !fp4_ld_ok(M, N, ldy))
         return BITNET_ERR_INVALID_ARG;
@@ -1344,8 +1461,8 @@ BITNET_API int bitnet_fp4_linear(const void *x, int xdtype, int64_t ldx, const f
     if (!aligned(x, fp4_dtype_size(xdtype)) || !aligned(w, 16) || !aligned(w_scales, 16) || !aligned(y, 2) ||
         !aligned(ga, 4) || !aligned(gw, 4))
         return BITNET_ERR_ALIGNMENT;
-    const int64_t cb = round_up(bitnet_fp4_code_bytes(M, K), 256);
-    const int64_t need = K > 0 ? cb + bitnet_fp4_scale_bytes(M, K, format) : 0;
+    const int64_t cb = round_up(M * fp4_row_bytes(K), 256);
+    const int64_t need = M > kFp4FusedTokens && K > 0 ? cb + bitnet_fp4_scale_bytes(M, K, format) : 0;
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return BITNET_ERR_WORKSPACE;
     if (need > 0 && !aligned(workspace, 256)) return BITNET_ERR_ALIGNMENT;
     if (fp4_patches(M, K) > (1LL << 31) - 1) return BITNET_ERR_UNSUPPORTED;
@@ -1354,6 +1471,13 @@ BITNET_API int bitnet_fp4_linear(const void *x, int xdtype, int64_t ldx, const f
     if (rc != BITNET_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (K == 0) return fp4_zero(dev, y, ydtype, M, N, ldy, st);
+    if (M <= kFp4FusedTokens) {  // one launch
+        Fp4SmallArgs a = fp4_small_args(w_scales, ga, gw, y, ydtype, M, N, K, ldy);
+        a.x = x;
+        a.xtype = xdtype;
+        a.ldx = ldx;
+        return launch_fp4_small(dev, nullptr, w, format, a, st);
+    }
     uint8_t *codes = static_cast<uint8_t *>(workspace), *scales = codes + cb;
     if ((rc = launch_fp4_quant(x, xdtype, M, K, ldx, format, ga, codes, scales, st)) != BITNET_OK) return rc;
     return launch_fp4_gemm(dev, codes, scales, ga, w, w_scales, gw, format, y, ydtype, M, N, K, ldy, st);

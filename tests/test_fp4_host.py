@@ -32,7 +32,8 @@ def test_sizes(lib):
         for fmt in (ref.MX, ref.NV):
             assert bn.bitnet_fp4_scale_bytes(rows, K, fmt) == ref.pad_up(rows, 128) * Kp // ref.BLOCK[fmt]
             ws = bn.bitnet_fp4_workspace_bytes(rows, 64, K, fmt)
-            assert ws >= rows * Kp // 2 + ref.pad_up(rows, 128) * Kp // ref.BLOCK[fmt]
+            if rows > 16:  # the linear layer's codes and scales
+                assert ws >= rows * Kp // 2 + ref.pad_up(rows, 128) * Kp // ref.BLOCK[fmt]
             assert ws == bn.bitnet_fp4_workspace_bytes(rows, 64, K, fmt)
     assert bn.bitnet_fp4_code_bytes(0, 64) == 0 and bn.bitnet_fp4_scale_bytes(5, 0, ref.MX) == 0
     assert lib.bitnet_fp4_code_bytes(-1, 4) == -1
@@ -94,9 +95,8 @@ def test_tensor_scale_refusals(no_gpu):
 
 def test_product_refusals(no_gpu):
     f = no_gpu.bitnet_fp4_gemm
-    need = bn.bitnet_fp4_workspace_bytes(3, 8, 64, 0)
-    names = ["a", "sa", "ga", "w", "sw", "gw", "fmt", "y", "dt", "M", "N", "K", "ldy", "ws", "wsb"]
-    ok = [A, A, NULL, A, A, NULL, 0, A, 0, 3, 8, 64, 8, WS, need]
+    names = ["a", "sa", "ga", "w", "sw", "gw", "fmt", "y", "dt", "M", "N", "K", "ldy"]
+    ok = [A, A, NULL, A, A, NULL, 0, A, 0, 3, 8, 64, 8]
 
     def call(**change):
         a = list(ok)
