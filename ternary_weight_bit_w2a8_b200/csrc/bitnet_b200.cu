@@ -1048,17 +1048,24 @@ int launch_fp4_small(DeviceInfo *dev, const uint8_t *codes, const uint8_t *w, in
     });
 }
 
-// Weight rows per tile of the pair kernel: the width whose rounds over the 74
-// pairs take the fewest cycles, a 256-k stage counted at what an SM loads for
-// it (64 bytes a cycle) and a tile's start and end with the rest.
-int fp4_pair_width(int64_t M, int64_t N, int64_t K) {
+// Weight rows per tile of the pair kernel: the width whose rounds over the
+// B200's 74 pairs take the fewest cycles.  Measured: a 256-k stage takes 352,
+// 425, 483 and 600 cycles for 64, 128, 192 and 256 rows (what an SM loads for
+// it, at 60 to 65 bytes a cycle; the MMAs take twice the rows), with NV scales
+// 192 and 256 rows 520 and 625; a tile costs some 500 more, one of 256 rows,
+// whose single accumulator has to be emptied first, 1500.  2048 x 2560 x 6912
+// NV takes 21.6 us with 192 rows, 23.4 with 256; 2048 x 9472 x 10240 takes
+// 81.0 and 69.6.
+int fp4_pair_width(int64_t M, int64_t N, int64_t K, int format) {
+    constexpr int kWidths[4] = {256, 192, 128, 64};
+    constexpr int kStage[2][4] = {{600, 483, 425, 352}, {625, 520, 425, 352}};
     const int64_t nk = ceil_div(k_pad(K), kFp4StageK), tm = ceil_div(M, 256);
     int best = 256;
     int64_t cost = INT64_MAX;
-    for (int bt = 256; bt >= 64; bt /= 2) {
-        const int64_t stage = bt == 256 ? 608 : (bt == 128 ? 448 : 384), end = bt == 256 ? 800 : 200;
-        const int64_t c = ceil_div(tm * ceil_div(N, bt), 74) * (nk * stage + end);
-        if (c < cost) cost = c, best = bt;
+    for (int i = 0; i < 4; ++i) {
+        const int64_t rounds = ceil_div(tm * ceil_div(N, kWidths[i]), 74);
+        const int64_t c = rounds * (nk * kStage[format == BITNET_FP4_MX ? 0 : 1][i] + (i == 0 ? 1500 : 500));
+        if (c < cost) cost = c, best = kWidths[i];
     }
     return best;
 }
@@ -1078,7 +1085,7 @@ int launch_fp4_pair_variant(DeviceInfo *dev, const CUtensorMap &amap, const CUte
 int launch_fp4_pair(DeviceInfo *dev, const uint8_t *codes, const uint8_t *sa, const float *ga, const uint8_t *w,
                     const uint8_t *sw, const float *gw, int format, void *y, int dtype, int64_t M, int64_t N, int64_t K,
                     int64_t ldy, cudaStream_t st) {
-    const int BT = fp4_pair_width(M, N, K);
+    const int BT = fp4_pair_width(M, N, K, format);
     if (ceil_div(M, 256) * ceil_div(N, BT) > (int64_t)1 << 30) return BITNET_ERR_UNSUPPORTED;
     const int64_t tiles = fp4_scale_tiles(K, format);
     if ((ceil_div(M, 128) + 1) * tiles > INT32_MAX || (ceil_div(N, 128) + 1) * tiles > INT32_MAX || N > INT32_MAX)
@@ -1099,12 +1106,13 @@ int launch_fp4_pair(DeviceInfo *dev, const uint8_t *codes, const uint8_t *sa, co
     a.ytype = dtype;
     a.tiles_m = (int)ceil_div(M, 256);
     a.tiles_n = (int)ceil_div(N, BT);
-    a.vec = aligned(y, 32) && ldy % 16 == 0;
+    a.vec = aligned(y, 16) && ldy % 8 == 0;
     return fp4_by_format(format, [&](auto fm) {
         constexpr int F = decltype(fm)::value;
         switch (BT) {
             case 64: return launch_fp4_pair_variant<F, 64>(dev, amap, wmap, samap, swmap, a, st);
             case 128: return launch_fp4_pair_variant<F, 128>(dev, amap, wmap, samap, swmap, a, st);
+            case 192: return launch_fp4_pair_variant<F, 192>(dev, amap, wmap, samap, swmap, a, st);
             default: return launch_fp4_pair_variant<F, 256>(dev, amap, wmap, samap, swmap, a, st);
         }
     });

@@ -29,6 +29,21 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
         : "memory");
 }
 
+// One lane of a converged warp, always the same one.  The loops that issue
+// MMAs and copies run on the whole warp and issue under this: with `lane == 0`
+// in its place the compiler cannot see that one thread issues, and a 256-k
+// stage of the pair kernel below took 727 cycles instead of its 512.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Whole-warp bounded wait: every lane gives up or none does.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+    return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_flag)) != 0;
+}
+
 // Instruction descriptor: e2m1 x e2m1, fp32 accumulate, K-major, M = m, N = n,
 // scale type 1 (e8m0) or 0 (e4m3); the two scale ids (which byte of a column
 // holds the first scale) are added per instruction.
@@ -59,11 +74,15 @@ __device__ __forceinline__ void umma_fp4(uint32_t d, uint64_t a, uint64_t b, uin
             : "memory");
 }
 
-// One scale tile from shared memory (512 bytes, 16-byte aligned) to four
-// tensor-memory columns, repeated over the four lane quarters.
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint32_t saddr) {
-    // unswizzled: 8-row groups of 16-byte rows, 128 bytes from group to group
-    const uint64_t desc = (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+// Descriptor of a scale tile in shared memory (512 bytes, 16-byte aligned),
+// unswizzled: 8-row groups of 16-byte rows, 128 bytes from group to group.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+}
+
+// One scale tile to four tensor-memory columns, repeated over the four lane
+// quarters.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
@@ -225,11 +244,11 @@ __global__ void __launch_bounds__(kFp4Threads, 2)
     pdl_launch_dependents();
 
     if (warp == 0) {
-        if (lane == 0) {
-            int i = 0;
-            for (; i < n_i; ++i) {
-                const int s = i % S, gi = i0 + i;
-                if (i >= S && !tc_wait(&empty[s], (uint32_t)(i / S - 1) & 1u, abort_flag)) break;
+        int i = 0;
+        for (; i < n_i; ++i) {
+            const int s = i % S, gi = i0 + i;
+            if (i >= S && !warp_wait(&empty[s], (uint32_t)(i / S - 1) & 1u, abort_flag)) break;
+            if (elect_one()) {
                 uint8_t *st = sm + s * L::kStage;
                 const uint32_t sb = scale_bytes(gi);
                 mbar_arrive_expect_tx(&full[s], QX ? L::kPBytes + sb : L::kPBytes + L::kQBytes + 2 * sb);
@@ -241,26 +260,24 @@ __global__ void __launch_bounds__(kFp4Threads, 2)
                     bulk_load(ss + L::kS, a.sa + (int64_t)gi * L::kS, sb, &full[s]);
                 }
             }
-            // no copy may still be landing when the CTA leaves (QX: a stage's
-            // barrier also waits for the quantisers, which stop on an abort;
-            // the wait is bounded)
-            for (int j = i - S < 0 ? 0 : i - S; j < i; ++j) mbar_wait_bounded(&full[j % S], (uint32_t)(j / S) & 1u);
+            __syncwarp();
         }
-        __syncwarp();
+        // no copy may still be landing when the CTA leaves (QX: a stage's
+        // barrier also waits for the quantisers, which stop on an abort; the
+        // wait is bounded)
+        for (int j = i - S < 0 ? 0 : i - S; j < i; ++j) mbar_wait_bounded(&full[j % S], (uint32_t)(j / S) & 1u);
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = fp4_idesc(FMT, kFp4Rows, BT);
-            bool ok = true;
-            for (int i = 0; i < n_i; ++i) {
-                const int s = i % S;
-                // two sets of scale columns take turns: the MMAs that read this
-                // one, two stages ago, are done
-                if (!tc_wait(&full[s], (uint32_t)(i / S) & 1u, abort_flag) ||
-                    (i >= 2 && !tc_wait(&empty[(i - 2) % S], (uint32_t)((i - 2) / S) & 1u, abort_flag))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
+        constexpr uint32_t idesc = fp4_idesc(FMT, kFp4Rows, BT);
+        bool ok = true;
+        for (int i = 0; i < n_i; ++i) {
+            const int s = i % S;
+            // two sets of scale columns take turns: the MMAs that read this
+            // one, two stages ago, are done
+            ok = warp_wait(&full[s], (uint32_t)(i / S) & 1u, abort_flag) &&
+                 (i < 2 || warp_wait(&empty[(i - 2) % S], (uint32_t)((i - 2) / S) & 1u, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
                 const uint32_t pa = smem_u32(sm + s * L::kStage), qa = pa + L::kPBytes;
                 const uint32_t spa = qa + L::kQBytes, sqa = spa + L::kS;
                 const uint32_t cp = tmem + (uint32_t)(BT + (i & 1) * L::kSlotCols), cq = cp + 4 * L::kTiles;
@@ -268,8 +285,8 @@ __global__ void __launch_bounds__(kFp4Threads, 2)
                 const int steps = (int)(left < 4 ? left : 4);
 #pragma unroll
                 for (int t = 0; t < L::kTiles; ++t) {
-                    tmem_cp_scales(cp + 4 * t, spa + t * kFp4TileBytes);
-                    tmem_cp_scales(cq + 4 * t, sqa + t * kFp4TileBytes);
+                    tmem_cp_scales(cp + 4 * t, scale_desc(spa + t * kFp4TileBytes));
+                    tmem_cp_scales(cq + 4 * t, scale_desc(sqa + t * kFp4TileBytes));
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -282,14 +299,12 @@ __global__ void __launch_bounds__(kFp4Threads, 2)
                 }
                 umma_commit(&empty[s]);
             }
-            if (ok) {
-                umma_commit(done);
-            } else {
-                umma_commit(drain);  // the MMAs issued so far end before tensor memory is freed
-                mbar_wait_bounded(drain, 0);
-            }
+            __syncwarp();
         }
+        if (elect_one()) umma_commit(ok ? done : drain);
         __syncwarp();
+        // on an abort the MMAs issued so far end before tensor memory is freed
+        if (!ok) mbar_wait_bounded(drain, 0);
     } else {
         if (QX) {
             // warp w of four takes tokens w, w + 4, ...; a lane 8 of a stage's 256 k.  The next stage's values are
@@ -307,7 +322,7 @@ __global__ void __launch_bounds__(kFp4Threads, 2)
             for (int i = 0; i < n_i; ++i) {
                 const int s = i % S;
                 // the lanes stop together (they shuffle below)
-                if (i >= S && !__all_sync(0xffffffffu, tc_wait(&empty[s], (uint32_t)(i / S - 1) & 1u, abort_flag))) break;
+                if (i >= S && !warp_wait(&empty[s], (uint32_t)(i / S - 1) & 1u, abort_flag)) break;
                 uint8_t *q = sm + s * L::kStage + L::kPBytes, *sq = q + L::kQBytes + L::kS;
                 float v[R][8];
 #pragma unroll
@@ -348,7 +363,7 @@ __global__ void __launch_bounds__(kFp4Threads, 2)
         const int quarter = warp & 3;
         const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16);
         const int row = quarter * 32 + lane;
-        if (__all_sync(0xffffffffu, tc_wait(done, 0u, abort_flag))) {
+        if (warp_wait(done, 0u, abort_flag)) {
             tc_fence_after();
             const float g = (a.ga != nullptr ? *a.ga : 1.0f) * (a.gw != nullptr ? *a.gw : 1.0f);
             const int64_t n = (int64_t)tile * kFp4Rows + row;

@@ -13,7 +13,7 @@
 // and completes on the first CTA's barrier; warp 1 of the first CTA issues the
 // scale copies and MMAs of both; eight epilogue warps per CTA empty the
 // accumulators into registers as 16-bit values, release them and store rows
-// while the next tile runs (two accumulators where they fit: BT <= 128).
+// while the next tile runs (two accumulators where they fit: BT <= 192).
 #pragma once
 
 #include "fp4_gemm.cuh"
@@ -29,25 +29,32 @@ struct Fp4PairArgs {
     void *y;
     int ytype;
     int tiles_m, tiles_n;  // 256-token and BT-row tiles
-    int vec;               // rows of y start on 32-byte boundaries
+    int vec;               // rows of y start on 16-byte boundaries
 };
 
 template <int FMT, int BT>
 struct Fp4Pair {
     static constexpr int kTiles = FMT == BITNET_FP4_MX ? 2 : 4;  // scale tiles per stage and 128 rows
-    static constexpr int kBands = (BT + 127) / 128;              // 128-row bands of weight scales
-    static constexpr int kAcc = BT <= 128 ? 2 : 1;               // accumulators
+    // A tile starts on a multiple of 64 rows, so its weight scales may start in the middle of a 128-row band: two
+    // tensor-memory columns in.  (An odd column, as tiles of 96 or 160 rows would need, is refused by the MMA.)
+    static constexpr int kBands = (BT + 127) / 128;
+    static constexpr int kAcc = BT <= 192 ? 2 : 1;               // accumulators
     static constexpr int kABytes = 128 * 128, kWBytes = BT / 2 * 128, kS = kTiles * kFp4TileBytes;
     static constexpr int kStage = kABytes + kWBytes + (1 + kBands) * kS;
-    static constexpr int kOut = kFp4PairEpiWarps * 32 * 17 * 4;  // per-warp transposition of ragged outputs
-    static constexpr int kStages = (222 * 1024 - kOut) / kStage < 8 ? (222 * 1024 - kOut) / kStage : 8;
+    static constexpr int kOut = kFp4PairEpiWarps * 4096;         // a box of 32 rows x 128 bytes of y per warp
+    static constexpr int kStages = (224 * 1024 - kOut) / kStage < 8 ? (224 * 1024 - kOut) / kStage : 8;
     static constexpr int kOutAt = kStages * kStage;
     static constexpr int kBars = kOutAt + kOut;
     static constexpr int kBytes = kBars + (2 * kStages + 5) * 8 + 16;
-    static constexpr int kSlotCols = 4 * kTiles * (1 + kBands);  // tensor-memory columns of a stage's scales
-    static constexpr int kNeed = kAcc * BT + 2 * kSlotCols;
+    // Tensor-memory columns of a stage's scales, and how many stages' fit beside the accumulators.  With as many as
+    // shared-memory stages, a stage's columns are free when its codes are; with fewer (192 columns of NV: 2) the issuer
+    // waits for older MMAs, which cost it 190 cycles a stage.
+    static constexpr int kSlotCols = 4 * kTiles * (1 + kBands);
+    static constexpr int kFit = (512 - kAcc * BT) / kSlotCols;
+    static constexpr int kSlots = kFit < kStages ? kFit : kStages;
+    static constexpr int kNeed = kAcc * BT + kSlots * kSlotCols;
     static constexpr int kCols = kNeed <= 256 ? 256 : 512;
-    static_assert(kNeed <= 512 && kStages >= 3 && BT % 64 == 0 && BT <= 256, "tile");
+    static_assert(kNeed <= 512 && kStages >= 3 && kSlots >= 2 && BT % 64 == 0 && BT <= 256, "tile");
     static_assert(kStage % 1024 == 0 && kWBytes % 1024 == 0, "swizzled rows");
 };
 
@@ -82,8 +89,7 @@ __device__ __forceinline__ void umma_fp4_pair(uint32_t d, uint64_t a, uint64_t b
 }
 
 // Each CTA of the pair copies the tile at this offset of its own shared memory.
-__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint32_t saddr) {
-    const uint64_t desc = (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t desc) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
@@ -114,19 +120,30 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *v) {
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // Two fp32 values as 16-bit ones, a in the low half.
-__device__ __forceinline__ uint32_t pack2(float a, float b, int dtype) {
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
     uint32_t r;
-    if (dtype == BITNET_FP16)
+    if (DT == BITNET_FP16)
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     else
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
 
-__device__ __forceinline__ void stg_32(void *p, const uint32_t *v) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
+// 32 * groups (1 or 2) accumulators of a lane times gs as a row of its warp's box: 128-byte
+// rows, 16-byte piece w of row r at piece w ^ (r % 8).
+template <int DT>
+__device__ __forceinline__ void box_rows(uint8_t *box, const uint32_t *f, int groups, float gs, int lane) {
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        if (w >= 4 * groups) break;
+        uint32_t t[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            t[i] = pack2<DT>(__fmul_rn(__uint_as_float(f[8 * w + 2 * i]), gs),
+                             __fmul_rn(__uint_as_float(f[8 * w + 2 * i + 1]), gs));
+        *reinterpret_cast<uint4 *>(box + lane * 128 + ((w ^ (lane & 7)) << 4)) = make_uint4(t[0], t[1], t[2], t[3]);
+    }
 }
 
 template <int FMT, int BT>
@@ -186,19 +203,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
 
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA producer
-        if (lane == 0) {
-            int g = 0;  // stages over all of this pair's tiles
-            bool ok = true;
-            for (int u = pair; ok && u < units; u += pairs) {
-                const int tm = u % a.tiles_m, tn = u / a.tiles_m;
-                const int m0 = tm * 256 + (int)rank * 128;
-                const int64_t n0 = (int64_t)tn * BT;
-                for (int i = 0; i < nk; ++i, ++g) {
-                    const int s = g % S;
-                    if (g >= S && !tc_wait(&empty[s], (uint32_t)(g / S - 1) & 1u, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
+        int g = 0;  // stages over all of this pair's tiles
+        bool ok = true;
+        for (int u = pair; ok && u < units; u += pairs) {
+            const int tm = u % a.tiles_m, tn = u / a.tiles_m;
+            const int m0 = tm * 256 + (int)rank * 128;
+            const int64_t n0 = (int64_t)tn * BT;
+            for (int i = 0; i < nk; ++i, ++g) {
+                const int s = g % S;
+                if (g >= S && !warp_wait(&empty[s], (uint32_t)(g / S - 1) & 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
                     uint8_t *st = sm + s * L::kStage;
                     const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * L::kStage);
@@ -210,118 +227,138 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
                     for (int b = 0; b < L::kBands; ++b)
                         tma_load_pair(ss + (1 + b) * L::kS, &swmap, 0, (int)(n0 / 128 + b) * tiles + i * L::kTiles, bar);
                 }
+                __syncwarp();
             }
-            // no copy may still be landing when the pair leaves (the first CTA
-            // sees both CTAs' copies; they leave together)
-            if (rank == 0)
-                for (int j = g - S < 0 ? 0 : g - S; j < g; ++j) mbar_wait_bounded(&full[j % S], (uint32_t)(j / S) & 1u);
         }
-        __syncwarp();
+        // no copy may still be landing when the pair leaves (the first CTA
+        // sees both CTAs' copies; they leave together)
+        if (rank == 0)
+            for (int j = g - S < 0 ? 0 : g - S; j < g; ++j) mbar_wait_bounded(&full[j % S], (uint32_t)(j / S) & 1u);
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
-        if (rank == 0 && lane == 0) {
+        // One thread; what it does per stage has to stay below the MMAs' 2 BT cycles.
+        if (rank == 0 && elect_one()) {
             constexpr uint32_t idesc = fp4_idesc(FMT, 256, BT);
+            const uint32_t base = smem_u32(sm);
+            const uint64_t a0 = umma_desc_sw128(base), w0 = umma_desc_sw128(base + L::kABytes);
+            const uint64_t s0 = scale_desc(base + L::kABytes + L::kWBytes);
+            const int full_stages = (int)(kp / kFp4StageK);  // the last stage may hold 128 k only
             bool ok = true;
-            int g = 0, li = 0;
+            int s = 0, slot = 0, g = 0, li = 0;
+            uint32_t phase = 0;
             for (int u = pair; ok && u < units; u += pairs, ++li) {
                 const int d = li % L::kAcc;
                 if (li >= L::kAcc && !tc_wait(&acc_empty[d], (uint32_t)(li / L::kAcc - 1) & 1u, abort_flag)) {
                     ok = false;
                     break;
                 }
-                tc_fence_after();
                 const uint32_t dt = tmem + (uint32_t)(d * BT);
-                // a 64-row tile starts in the middle of a 128-row band
-                const uint32_t off = (uint32_t)(((int64_t)(u / a.tiles_m) * BT % 128) / 32);
+                // rows into the first band of weight scales: 32 to a column
+                const uint32_t off = BT % 128 == 0 ? 0 : (uint32_t)((u / a.tiles_m) * BT % 128) / 32;
                 for (int i = 0; i < nk; ++i, ++g) {
-                    const int s = g % S;
-                    if (!tc_wait(&full[s], (uint32_t)(g / S) & 1u, abort_flag) ||
-                        (g >= 2 && !tc_wait(&empty[(g - 2) % S], (uint32_t)((g - 2) / S) & 1u, abort_flag))) {
+                    if (!tc_wait(&full[s], phase, abort_flag) ||
+                        (L::kSlots < S && g >= L::kSlots &&
+                         !tc_wait(&empty[(g - L::kSlots) % S], (uint32_t)((g - L::kSlots) / S) & 1u, abort_flag))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t aa = smem_u32(sm + s * L::kStage), wa = aa + L::kABytes;
-                    const uint32_t saa = wa + L::kWBytes, swa = saa + L::kS;
-                    const uint32_t ca = tmem + (uint32_t)(L::kAcc * BT + (g & 1) * L::kSlotCols), cw = ca + 4 * L::kTiles;
-                    const int64_t left = (kp - (int64_t)i * kFp4StageK) / 64;
-                    const int steps = (int)(left < 4 ? left : 4);
+                    const uint64_t at = (uint64_t)(s * (L::kStage >> 4));
+                    const uint32_t ca = tmem + (uint32_t)(L::kAcc * BT + slot * L::kSlotCols), cw = ca + 4 * L::kTiles;
+                    const bool whole = i < full_stages;
 #pragma unroll
                     for (int t = 0; t < L::kTiles; ++t) {
-                        tmem_cp_scales_pair(ca + 4 * t, saa + t * kFp4TileBytes);
+                        if (t < L::kTiles / 2 || whole) {
+                            tmem_cp_scales_pair(ca + 4 * t, s0 + at + (uint64_t)(t * kFp4TileBytes >> 4));
 #pragma unroll
-                        for (int b = 0; b < L::kBands; ++b)
-                            tmem_cp_scales_pair(cw + 4 * (t * L::kBands + b), swa + b * L::kS + t * kFp4TileBytes);
+                            for (int b = 0; b < L::kBands; ++b)
+                                tmem_cp_scales_pair(cw + 4 * (t * L::kBands + b),
+                                                    s0 + at + (uint64_t)(((1 + b) * L::kS + t * kFp4TileBytes) >> 4));
+                        }
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        if (j < steps) {
-                            const int t = FMT == BITNET_FP4_MX ? j >> 1 : j;
-                            const int id = FMT == BITNET_FP4_MX ? (j & 1) * 2 : 0;
-                            umma_fp4_pair<FMT>(dt, umma_desc_sw128(aa + 32 * j), umma_desc_sw128(wa + 32 * j),
-                                               idesc | fp4_scale_id(id), ca + 4 * t, cw + 4 * t * L::kBands + off,
-                                               (i > 0 || j > 0) ? 1u : 0u);
-                        }
+                        const int t = FMT == BITNET_FP4_MX ? j >> 1 : j;
+                        const int id = FMT == BITNET_FP4_MX ? (j & 1) * 2 : 0;
+                        if (j < 2 || whole)
+                            umma_fp4_pair<FMT>(dt, a0 + at + 2 * j, w0 + at + 2 * j, idesc | fp4_scale_id(id), ca + 4 * t,
+                                               cw + 4 * t * L::kBands + off, j > 0 ? 1u : (uint32_t)(i > 0));
                     }
                     umma_commit_pair(&empty[s]);
+                    if (++s == S) s = 0, phase ^= 1;
+                    if (++slot == L::kSlots) slot = 0;
                 }
                 if (ok) umma_commit_pair(&acc_full[d]);
             }
             if (!ok) {
-                umma_commit_pair(drain);  // the MMAs issued so far end before tensor memory is freed
+                // the MMAs issued so far end before tensor memory is freed
+                umma_commit_pair(drain);
                 mbar_wait_bounded(drain, 0);
             }
         }
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- epilogue
-        constexpr int kCw = BT / 2;  // columns per warp: two warps share a lane quarter
+        // Two warps share a lane quarter: the first takes the first half of the tile's 32-column groups (rounded up),
+        // the second the rest.  The accumulator is released as soon as its values are in registers; they are put
+        // down as 16-bit values 64 columns at a time as 128-byte rows of shared memory (16-byte pieces swizzled, so that neither the
+        // lanes' rows nor a row's pieces share banks) and stored from there, whole rows of lines at a time.
+        constexpr int kGroups = BT / 32, kMost = (kGroups + 1) / 2;
         const int quarter = warp & 3, half = (warp - 2) >> 2;
-        const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * kCw);
-        uint32_t *buf = reinterpret_cast<uint32_t *>(sm + L::kOutAt) + (warp - 2) * 32 * 17;
+        const int groups = half == 0 ? kMost : kGroups - kMost;
+        const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * kMost * 32);
+        uint8_t *box = sm + L::kOutAt + (warp - 2) * 4096;
         const float gs = (a.ga != nullptr ? *a.ga : 1.0f) * (a.gw != nullptr ? *a.gw : 1.0f);
         int li = 0;
         for (int u = pair; u < units; u += pairs, ++li) {
             const int d = li % L::kAcc;
-            if (!__all_sync(0xffffffffu, tc_wait(&acc_full[d], (uint32_t)(li / L::kAcc) & 1u, abort_flag))) break;
+            if (!warp_wait(&acc_full[d], (uint32_t)(li / L::kAcc) & 1u, abort_flag)) break;
             tc_fence_after();
-            // 64 columns at a time, kept as 16-bit pairs
-            uint32_t v[kCw / 2];
+            uint32_t f[32 * kMost];
 #pragma unroll
-            for (int c0 = 0; c0 < kCw; c0 += 64) {
-                uint32_t f[kCw < 64 ? kCw : 64];
-#pragma unroll
-                for (int c = 0; c < kCw - c0 && c < 64; c += 32) tmem_ld32(t0 + (uint32_t)(d * BT + c0 + c), f + c);
-                tmem_wait_ld();
-#pragma unroll
-                for (int c = 0; c < kCw - c0 && c < 64; c += 2)
-                    v[(c0 + c) / 2] =
-                        pack2(__fmul_rn(__uint_as_float(f[c]), gs), __fmul_rn(__uint_as_float(f[c + 1]), gs), a.ytype);
-            }
+            for (int c = 0; c < kMost; ++c)
+                if (c < groups) tmem_ld32(t0 + (uint32_t)(d * BT + 32 * c), f + 32 * c);
+            tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&acc_empty[d]), 0));
             const int tm = u % a.tiles_m;
-            const int64_t m0 = (int64_t)tm * 256 + rank * 128 + quarter * 32, n0 = (int64_t)(u / a.tiles_m) * BT + half * kCw;
-            if (a.vec && n0 + kCw <= a.N) {
-                uint16_t *yp = static_cast<uint16_t *>(a.y) + (m0 + lane) * a.ldy + n0;
-                if (m0 + lane < a.M) {
+            const int64_t m0 = (int64_t)tm * 256 + rank * 128 + quarter * 32;
+            const int64_t n0 = (int64_t)(u / a.tiles_m) * BT + half * kMost * 32;
+            const int rows = (int)(a.M - m0 < 32 ? a.M - m0 : 32);
+            uint16_t *y = static_cast<uint16_t *>(a.y) + m0 * a.ldy;
 #pragma unroll
-                    for (int c = 0; c < kCw; c += 16) stg_32(yp + c, v + c / 2);
-                }
-            } else {
-                // through shared memory, so that a store covers 32 columns of a row
+            for (int c = 0; c < kMost; c += 2) {
+                if (c >= groups) break;
+                const int pieces = c + 1 < groups ? 8 : 4;  // of 8 columns to a row
+                __syncwarp();                               // the rows of the last round have been read
+                if (a.ytype == BITNET_FP16)
+                    box_rows<BITNET_FP16>(box, f + 32 * c, kMost - c < 2 ? 1 : 2, gs, lane);
+                else
+                    box_rows<BITNET_BF16>(box, f + 32 * c, kMost - c < 2 ? 1 : 2, gs, lane);
+                __syncwarp();
+                const int64_t nb = n0 + 32 * c;
+                if (a.vec) {
+                    const int w = lane & (pieces - 1), step = 32 / pieces;
+                    const int64_t n = nb + 8 * w;
+                    for (int r = lane / pieces; r < rows; r += step) {
+                        const uint4 t = *reinterpret_cast<const uint4 *>(box + r * 128 + ((w ^ (r & 7)) << 4));
+                        uint16_t *yp = y + r * a.ldy + n;
+                        if (n + 8 <= a.N) {
+                            *reinterpret_cast<uint4 *>(yp) = t;
+                        } else {
+                            const uint32_t q[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
-                for (int c = 0; c < kCw; c += 32) {
-                    __syncwarp();
-#pragma unroll
-                    for (int w = 0; w < 16; ++w) buf[lane * 17 + w] = v[c / 2 + w];
-                    __syncwarp();
-                    const int64_t n = n0 + c + lane;
-                    for (int r = 0; r < 32; ++r)
-                        if (m0 + r < a.M && n < a.N)
-                            static_cast<uint16_t *>(a.y)[(m0 + r) * a.ldy + n] =
-                                reinterpret_cast<const uint16_t *>(buf + r * 17)[lane];
+                            for (int e = 0; e < 8; ++e)
+                                if (n + e < a.N) yp[e] = (uint16_t)(q[e >> 1] >> (16 * (e & 1)));
+                        }
+                    }
+                } else {
+                    for (int r = 0; r < rows; ++r)
+                        for (int e = lane; e < 8 * pieces; e += 32)
+                            if (nb + e < a.N)
+                                y[r * a.ldy + nb + e] =
+                                    *reinterpret_cast<const uint16_t *>(box + r * 128 + (((e >> 3) ^ (r & 7)) << 4) + 2 * (e & 7));
                 }
             }
         }
