@@ -226,9 +226,9 @@ BITNET_API int64_t bitnet_fp4_code_bytes(int64_t rows, int64_t K);
 BITNET_API int64_t bitnet_fp4_scale_bytes(int64_t rows, int64_t K, int format);
 
 /*
- * Workspace bytes that bitnet_fp4_tensor_scale (M = its rows, any N) and
- * bitnet_fp4_linear need for an M x N x K problem (the larger of the two), or
- * -1 for invalid sizes or an unknown format.  Depends only on its arguments.
+ * Workspace bytes that bitnet_fp4_linear needs for an M x N x K problem, or -1
+ * for invalid sizes or an unknown format.  Depends only on its arguments; 0 up
+ * to 16 tokens.
  */
 BITNET_API int64_t bitnet_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K, int format);
 
@@ -238,11 +238,9 @@ BITNET_API int64_t bitnet_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K, i
  *   x         device, dtype [rows, K], row stride ldx >= K elements, aligned to
  *             its element
  *   g         device, 1 float (output)
- *   workspace device, >= bitnet_fp4_workspace_bytes(rows, 1, K, format) bytes,
- *             256-byte aligned
  */
 BITNET_API int bitnet_fp4_tensor_scale(const void *x, int dtype, int64_t rows, int64_t K, int64_t ldx, float *g,
-                                       void *workspace, int64_t workspace_bytes, void *stream);
+                                       void *stream);
 
 /*
  * Quantisation.  z = fl32(x * fl32(1 / g)); per block, with top = max |z|,

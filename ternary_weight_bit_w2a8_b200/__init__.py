@@ -49,7 +49,7 @@ _SIGNATURES = {
     "bitnet_fp4_code_bytes": (_i64, [_i64, _i64]),
     "bitnet_fp4_scale_bytes": (_i64, [_i64, _i64, _int]),
     "bitnet_fp4_workspace_bytes": (_i64, [_i64, _i64, _i64, _int]),
-    "bitnet_fp4_tensor_scale": (ctypes.c_int, [_p, _int, _i64, _i64, _i64, _p, _p, _i64, _p]),
+    "bitnet_fp4_tensor_scale": (ctypes.c_int, [_p, _int, _i64, _i64, _i64, _p, _p]),
     "bitnet_fp4_quant": (ctypes.c_int, [_p, _int, _i64, _i64, _i64, _int, _p, _p, _p, _p]),
     "bitnet_fp4_dequant": (ctypes.c_int, [_p, _p, _i64, _i64, _int, _p, _p, _int, _i64, _p]),
     "bitnet_fp4_gemm": (ctypes.c_int, [_p, _p, _p, _p, _p, _p, _int, _p, _int, _i64, _i64, _i64, _i64, _p]),
@@ -322,11 +322,12 @@ def _scale_bytes(rows, K, fmt):
 
 
 def _matrix(codes, scales, K, fmt, index, name):
-    """Pointers of a quantised matrix [rows, K]."""
-    if codes.dim() != 2 or codes.shape[1] != -(-K // 128) * 64:
-        raise ValueError(f"{name} must be [rows, {-(-K // 128) * 64}] for K = {K}, not {list(codes.shape)}")
+    """Pointers of a quantised matrix [rows, K], and its rows."""
+    shape = codes.shape
+    if len(shape) != 2 or shape[1] != (K + 127 >> 7) << 6:
+        raise ValueError(f"{name} must be [rows, {(K + 127 >> 7) << 6}] for K = {K}, not {list(shape)}")
     return (_flat(codes, name, _torch.uint8, index, 0),
-            _flat(scales, f"{name}'s scales", _torch.uint8, index, _scale_bytes(codes.shape[0], K, fmt)))
+            _flat(scales, name, _torch.uint8, index, _scale_bytes(shape[0], K, fmt)), shape[0])
 
 
 def bitnet_fp4_code_bytes(rows: int, K: int) -> int:
@@ -350,29 +351,19 @@ def bitnet_fp4_workspace_bytes(M: int, N: int, K: int, fmt: int) -> int:
     return n
 
 
-def _fp4_workspace(ws, M, N, K, fmt, t, index):
-    """The caller's workspace, or one of the size needed on t's device (none where none is needed)."""
-    if ws is None:
-        need = bitnet_fp4_workspace_bytes(M, N, K, fmt)
-        return t.new_empty(need, dtype=_torch.uint8) if need else None
-    _flat(ws, "ws", _torch.uint8, index, 0)
-    return ws
-
-
-def bitnet_fp4_tensor_scale(x, g=None, ws=None, stream=None):
+def bitnet_fp4_tensor_scale(x, g=None, stream=None):
     """Tensor scale of the NV format, max|x| / 2688 over the finite values of x -> float32 tensor [1]."""
     torch = _torch or _load_torch()
     index = _device_of(x, "x")
     if _elsewhere(index, stream):
         with _on(index, stream):
-            return bitnet_fp4_tensor_scale(x, g, ws)
+            return bitnet_fp4_tensor_scale(x, g)
     ldx = _rows(x, "x", index)
     rows, K = x.shape
     if g is None:
         g = x.new_empty(1, dtype=torch.float32)
-    ws = _fp4_workspace(ws, rows, 1, K, BITNET_FP4_NV, x, index)
     _check(lib().bitnet_fp4_tensor_scale(x.data_ptr(), _float_type(x.dtype, "x"), rows, K, ldx,
-                                         _flat(g, "g", torch.float32, index, 1), ws.data_ptr(), ws.numel(),
+                                         _flat(g, "g", torch.float32, index, 1),
                                          torch._C._cuda_getCurrentRawStream(index)), "bitnet_fp4_tensor_scale")
     return g
 
@@ -386,13 +377,16 @@ def bitnet_fp4_quant(x, fmt: int, g=None, codes=None, scales=None, stream=None):
             return bitnet_fp4_quant(x, fmt, g, codes, scales)
     ldx = _rows(x, "x", index)
     rows, K = x.shape
-    if codes is None:
-        codes = x.new_empty((rows, -(-K // 128) * 64), dtype=torch.uint8)
-    if scales is None:
-        scales = x.new_empty(_scale_bytes(rows, K, fmt), dtype=torch.uint8)
-    cp, sp = _matrix(codes, scales, K, fmt, index, "codes")
-    if codes.shape[0] != rows:
-        raise ValueError("codes and x differ in their rows")
+    if codes is None and scales is None:
+        codes = x.new_empty((rows, (K + 127 >> 7) << 6), dtype=torch.uint8)
+        scales = codes.new_empty(_scale_bytes(rows, K, fmt))
+        cp, sp = codes.data_ptr(), scales.data_ptr()
+    else:
+        if codes is None or scales is None:
+            raise ValueError("codes and scales are given together")
+        cp, sp, n = _matrix(codes, scales, K, fmt, index, "codes and scales")
+        if n != rows:
+            raise ValueError("codes and x differ in their rows")
     _check(lib().bitnet_fp4_quant(x.data_ptr(), _float_type(x.dtype, "x"), rows, K, ldx, fmt,
                                   _flat(g, "g", torch.float32, index, 1), cp, sp,
                                   torch._C._cuda_getCurrentRawStream(index)), "bitnet_fp4_quant")
@@ -406,11 +400,11 @@ def bitnet_fp4_dequant(codes, scales, K: int, fmt: int, g=None, dtype=None, y=No
     if _elsewhere(index, stream):
         with _on(index, stream):
             return bitnet_fp4_dequant(codes, scales, K, fmt, g, dtype, y)
-    cp, sp = _matrix(codes, scales, K, fmt, index, "codes")
-    rows = codes.shape[0]
+    cp, sp, rows = _matrix(codes, scales, K, fmt, index, "codes and scales")
     if y is None:
-        y = codes.new_empty((rows, K), dtype=dtype or torch.bfloat16)
-    ldy = _rows(y, "y", index, (rows, K))
+        y, ldy = codes.new_empty((rows, K), dtype=dtype or torch.bfloat16), K
+    else:
+        ldy = _rows(y, "y", index, (rows, K))
     _check(lib().bitnet_fp4_dequant(cp, sp, rows, K, fmt, _flat(g, "g", torch.float32, index, 1), y.data_ptr(),
                                     _float_type(y.dtype, "y"), ldy, torch._C._cuda_getCurrentRawStream(index)),
            "bitnet_fp4_dequant")
@@ -424,12 +418,12 @@ def bitnet_fp4_gemm(a, a_scales, w, w_scales, K: int, fmt: int, ga=None, gw=None
     if _elsewhere(index, stream):
         with _on(index, stream):
             return bitnet_fp4_gemm(a, a_scales, w, w_scales, K, fmt, ga, gw, dtype, y)
-    ap, asp = _matrix(a, a_scales, K, fmt, index, "a")
-    wp, wsp = _matrix(w, w_scales, K, fmt, index, "w")
-    M, N = a.shape[0], w.shape[0]
+    ap, asp, M = _matrix(a, a_scales, K, fmt, index, "a and a_scales")
+    wp, wsp, N = _matrix(w, w_scales, K, fmt, index, "w and w_scales")
     if y is None:
-        y = a.new_empty((M, N), dtype=dtype or torch.bfloat16)
-    ldy = _rows(y, "y", index, (M, N))
+        y, ldy = a.new_empty((M, N), dtype=dtype or torch.bfloat16), N
+    else:
+        ldy = _rows(y, "y", index, (M, N))
     _check(lib().bitnet_fp4_gemm(ap, asp, _flat(ga, "ga", torch.float32, index, 1), wp, wsp,
                                  _flat(gw, "gw", torch.float32, index, 1), fmt, y.data_ptr(),
                                  _float_type(y.dtype, "y"), M, N, K, ldy,
@@ -446,13 +440,15 @@ def bitnet_fp4_linear(x, w, w_scales, fmt: int, ga=None, gw=None, dtype=None, y=
             return bitnet_fp4_linear(x, w, w_scales, fmt, ga, gw, dtype, y, ws)
     ldx = _rows(x, "x", index)
     M, K = x.shape
-    wp, wsp = _matrix(w, w_scales, K, fmt, index, "w")
-    N = w.shape[0]
+    wp, wsp, N = _matrix(w, w_scales, K, fmt, index, "w and w_scales")
     if y is None:
-        y = x.new_empty((M, N), dtype=dtype or torch.bfloat16)
-    ldy = _rows(y, "y", index, (M, N))
-    if ws is not None or M > 16:  # fewer tokens need none
-        ws = _fp4_workspace(ws, M, N, K, fmt, x, index)
+        y, ldy = x.new_empty((M, N), dtype=dtype or torch.bfloat16), N
+    else:
+        ldy = _rows(y, "y", index, (M, N))
+    if ws is not None:
+        _flat(ws, "ws", torch.uint8, index, 0)
+    elif M > 16:  # fewer tokens need none
+        ws = x.new_empty(bitnet_fp4_workspace_bytes(M, N, K, fmt), dtype=torch.uint8)
     _check(lib().bitnet_fp4_linear(x.data_ptr(), _float_type(x.dtype, "x"), ldx,
                                    _flat(ga, "ga", torch.float32, index, 1), wp, wsp,
                                    _flat(gw, "gw", torch.float32, index, 1), fmt, y.data_ptr(),

@@ -950,12 +950,17 @@ inline int64_t fp4_patches(int64_t rows, int64_t K) {
     return ceil_div(rows, kFp4TileRows) * ceil_div(k_pad(K), kFp4PatchK);
 }
 
+// Whether rows of `esize`-byte elements start on 16-byte boundaries.
+inline bool fp4_rows_aligned(const void *p, int64_t ld, int esize) { return aligned(p, 16) && (ld * esize) % 16 == 0; }
+
 int launch_fp4_quant(const void *x, int dtype, int64_t rows, int64_t K, int64_t ldx, int format, const float *g,
                      uint8_t *codes, uint8_t *scales, cudaStream_t st) {
+    const bool al = fp4_rows_aligned(x, ldx, fp4_dtype_size(dtype));
     return fp4_by_type(dtype, [&](auto dt) {
         return fp4_by_format(format, [&](auto fm) {
-            using T = typename Fp4Type<decltype(dt)::value>::T;
-            return launched(launch_pdl(fp4_quant_kernel<decltype(dt)::value, decltype(fm)::value>,
+            constexpr int D = decltype(dt)::value, F = decltype(fm)::value;
+            using T = typename Fp4Type<D>::T;
+            return launched(launch_pdl(al ? fp4_quant_kernel<D, F, true> : fp4_quant_kernel<D, F, false>,
                                        dim3((unsigned)fp4_patches(rows, K)), dim3(kThreads), (size_t)0, st,
                                        static_cast<const T *>(x), rows, K, ldx, g, codes, scales));
         });
@@ -999,26 +1004,28 @@ bool fp4_code_map(CUtensorMap *m, const uint8_t *codes, int64_t rows, int64_t K,
 }
 
 // Tokens that the small kernel takes; more go to the pair kernel.
-constexpr int kFp4SmallTokens = 128;
+// (64 x 5120 x 5120 takes 8.2 us in the small kernel, 9.1 in the other; 128 x
+// 13824 x 2560 11.2 and 8.7).
+constexpr int kFp4SmallTokens = 64;
 
-// CTAs per weight tile of the small kernel: the split whose waves of CTAs (two
-// per SM) take the fewest stages, a CTA's start and end counted as two.  From
-// the sizes alone, so that the sums' grouping depends on nothing else.
+// CTAs per weight tile of the small kernel: as many as leave 240 CTAs or fewer
+// (a CTA lives some 3 us beside its loads, so more of them than the SMs hold at
+// once cost more than the shorter ranges of k save) and two stages to each.
+// Measured, in us, for 1, 2, 4 and 8: 1 x 2560 x 6912 10.9, 7.4, 5.5, 5.1;
+// 1 x 6912 x 2560 5.3, 5.2, 4.6, 8.1; 1 x 13824 x 5120 10.1, 9.5, 11.8, 14.9;
+// 1 x 55296 x 5120 23.2, 26.7, 34.4, 48.4.  From the sizes alone, so that the
+// sums' grouping depends on nothing else.
 int fp4_split(int64_t N, int64_t K) {
     const int64_t tiles = ceil_div(N, kFp4Rows), nk = ceil_div(k_pad(K), kFp4StageK);
-    int best = 1;
-    int64_t cost = INT64_MAX;
-    for (int s = 1; s <= kFp4MaxSplit && s <= nk; s *= 2) {
-        const int64_t c = ceil_div(tiles * s, 2 * 148) * (ceil_div(nk, s) + 2);
-        if (c < cost) cost = c, best = s;
-    }
-    return best;
+    int s = 1;
+    while (2 * s <= kFp4MaxSplit && tiles * 2 * s <= 240 && nk >= 4 * s) s *= 2;
+    return s;
 }
 
-template <int FMT, int BT, bool QX>
+template <int FMT, int BT, int XT>
 int launch_fp4_small_variant(DeviceInfo *dev, const CUtensorMap &wmap, const CUtensorMap &amap, const Fp4SmallArgs &a,
                              cudaStream_t st) {
-    auto kern = fp4_small_kernel<FMT, BT, QX>;
+    auto kern = fp4_small_kernel<FMT, BT, XT>;
     constexpr size_t smem = Fp4Small<FMT, BT>::kBytes + 1024;
     static std::atomic<uint64_t> set{0};
     if (!fp4_opt_in(dev, kern, smem, set)) return BITNET_ERR_CUDA;
@@ -1027,23 +1034,25 @@ int launch_fp4_small_variant(DeviceInfo *dev, const CUtensorMap &wmap, const CUt
     return launched(launch_pdl_cluster(kern, (unsigned)grid, kFp4Threads, (unsigned)a.split, smem, st, wmap, amap, a));
 }
 
-// codes == null: the tokens are quantised in the kernel (a.x).
-int launch_fp4_small(DeviceInfo *dev, const uint8_t *codes, const uint8_t *w, int format, Fp4SmallArgs a,
+// codes == null: the tokens are quantised in the kernel (a.x, of type xtype).
+int launch_fp4_small(DeviceInfo *dev, const uint8_t *codes, int xtype, const uint8_t *w, int format, Fp4SmallArgs a,
                      cudaStream_t st) {
     a.split = fp4_split(a.N, a.K);
-    const int BT = a.M <= 16 ? 16 : (a.M <= 32 ? 32 : (a.M <= 64 ? 64 : 128));
+    const int BT = a.M <= 16 ? 16 : (a.M <= 32 ? 32 : 64);
     CUtensorMap wmap, amap;
     memset(&amap, 0, sizeof(amap));
     if (!fp4_code_map(&wmap, w, a.N, a.K, kFp4Rows) || (codes != nullptr && !fp4_code_map(&amap, codes, a.M, a.K, BT)))
         return BITNET_ERR_CUDA;
     return fp4_by_format(format, [&](auto fm) {
         constexpr int F = decltype(fm)::value;
-        if (codes == nullptr) return launch_fp4_small_variant<F, kFp4FusedTokens, true>(dev, wmap, amap, a, st);
+        if (codes == nullptr)
+            return fp4_by_type(xtype, [&](auto xt) {
+                return launch_fp4_small_variant<F, kFp4FusedTokens, decltype(xt)::value>(dev, wmap, amap, a, st);
+            });
         switch (BT) {
-            case 16: return launch_fp4_small_variant<F, 16, false>(dev, wmap, amap, a, st);
-            case 32: return launch_fp4_small_variant<F, 32, false>(dev, wmap, amap, a, st);
-            case 64: return launch_fp4_small_variant<F, 64, false>(dev, wmap, amap, a, st);
-            default: return launch_fp4_small_variant<F, 128, false>(dev, wmap, amap, a, st);
+            case 16: return launch_fp4_small_variant<F, 16, kFp4Quantised>(dev, wmap, amap, a, st);
+            case 32: return launch_fp4_small_variant<F, 32, kFp4Quantised>(dev, wmap, amap, a, st);
+            default: return launch_fp4_small_variant<F, 64, kFp4Quantised>(dev, wmap, amap, a, st);
         }
     });
 }
@@ -1137,7 +1146,7 @@ int launch_fp4_gemm(DeviceInfo *dev, const uint8_t *a, const uint8_t *sa, const 
         return launch_fp4_pair(dev, a, sa, ga, w, sw, gw, format, y, dtype, M, N, K, ldy, st);
     Fp4SmallArgs s = fp4_small_args(sw, ga, gw, y, dtype, M, N, K, ldy);
     s.sa = sa;
-    return launch_fp4_small(dev, a, w, format, s, st);
+    return launch_fp4_small(dev, a, 0, w, format, s, st);
 }
 
 // y = 0 (K == 0).
@@ -1357,37 +1366,38 @@ BITNET_API int64_t bitnet_fp4_scale_bytes(int64_t rows, int64_t K, int format) {
 
 BITNET_API int64_t bitnet_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K, int format) {
     if (!sizes_ok(M, 1, K) || !sizes_ok(N, 1, K) || !fp4_format_ok(format)) return -1;
-    const int64_t scale = (int64_t)kFp4ScaleMaxBlocks * 4;
-    const int64_t linear =
-        M > kFp4FusedTokens && N > 0 ? round_up(M * fp4_row_bytes(K), 256) + bitnet_fp4_scale_bytes(M, K, format) : 0;
-    return linear > scale ? linear : scale;
+    if (M <= kFp4FusedTokens || N == 0) return 0;
+    return round_up(M * fp4_row_bytes(K), 256) + bitnet_fp4_scale_bytes(M, K, format);
 }
 
 BITNET_API int bitnet_fp4_tensor_scale(const void *x, int dtype, int64_t rows, int64_t K, int64_t ldx, float *g,
-                                       void *workspace, int64_t workspace_bytes, void *stream) {
+                                       void *stream) {
     if (!sizes_ok(rows, 1, K) || !fp4_dtype_ok(dtype) || !fp4_ld_ok(rows, K, ldx) || g == nullptr ||
         (rows * K > 0 && x == nullptr))
         return BITNET_ERR_INVALID_ARG;
     if (!aligned(x, fp4_dtype_size(dtype)) || !aligned(g, 4)) return BITNET_ERR_ALIGNMENT;
-    if (workspace == nullptr || workspace_bytes < (int64_t)kFp4ScaleMaxBlocks * 4) return BITNET_ERR_WORKSPACE;
-    if (!aligned(workspace, 256)) return BITNET_ERR_ALIGNMENT;
     DeviceInfo *dev = nullptr;
-    int rc = device_info(&dev);
+    const int rc = device_info(&dev);
     if (rc != BITNET_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    uint32_t *partial = static_cast<uint32_t *>(workspace);
-    int64_t blocks = ceil_div(rows * ceil_div(K, 8), kThreads);
-    if (blocks > kFp4ScaleMaxBlocks) blocks = kFp4ScaleMaxBlocks;
-    if (blocks > 0) {
-        rc = fp4_by_type(dtype, [&](auto dt) {
-            using T = typename Fp4Type<decltype(dt)::value>::T;
-            return launched(launch_pdl(fp4_absmax_kernel<decltype(dt)::value>, dim3((unsigned)blocks), dim3(kThreads),
-                                       (size_t)0, st, static_cast<const T *>(x), rows, K, ldx, partial));
-        });
-        if (rc != BITNET_OK) return rc;
+    if (ldx == K) {  // no gaps: one long row, so that no piece is a short one
+        K *= rows;
+        ldx = K;
+        rows = 1;
     }
-    return launched(launch_pdl(fp4_tensor_scale_kernel, dim3(1), dim3(kThreads), (size_t)0, st,
-                               (const uint32_t *)partial, (int)blocks, g));
+    return fp4_by_type(dtype, [&](auto dt) {
+        constexpr int D = decltype(dt)::value;
+        using T = typename Fp4Type<D>::T;
+        int64_t blocks = ceil_div(rows * ceil_div(K, kFp4ScalePiece<D>), kThreads / 32);
+        if (blocks > 4 * dev->sm_count) blocks = 4 * dev->sm_count;
+        if (blocks < 1) blocks = 1;
+        if (blocks > 1) {
+            const int rc1 = launched(launch_pdl(fp4_clear_kernel, dim3(1), dim3(1), (size_t)0, st, g));
+            if (rc1 != BITNET_OK) return rc1;
+        }
+        return launched(launch_pdl(fp4_tensor_scale_kernel<D>, dim3((unsigned)blocks), dim3(kThreads), (size_t)0, st,
+                                   static_cast<const T *>(x), rows, K, ldx, g));
+    });
 }
 
 BITNET_API int bitnet_fp4_quant(const void *x, int dtype, int64_t rows, int64_t K, int64_t ldx, int format,
@@ -1417,10 +1427,12 @@ BITNET_API int bitnet_fp4_dequant(const uint8_t *codes, const uint8_t *scales, i
     DeviceInfo *dev = nullptr;
     const int rc = device_info(&dev);
     if (rc != BITNET_OK) return rc;
+    const bool al = fp4_rows_aligned(y, ldy, fp4_dtype_size(dtype));
     return fp4_by_type(dtype, [&](auto dt) {
         return fp4_by_format(format, [&](auto fm) {
-            using T = typename Fp4Type<decltype(dt)::value>::T;
-            return launched(launch_pdl(fp4_dequant_kernel<decltype(dt)::value, decltype(fm)::value>,
+            constexpr int D = decltype(dt)::value, F = decltype(fm)::value;
+            using T = typename Fp4Type<D>::T;
+            return launched(launch_pdl(al ? fp4_dequant_kernel<D, F, true> : fp4_dequant_kernel<D, F, false>,
                                        dim3((unsigned)fp4_patches(rows, K)), dim3(kThreads), (size_t)0,
                                        static_cast<cudaStream_t>(stream), codes, scales, rows, K, g,
                                        static_cast<T *>(y), ldy));
@@ -1482,9 +1494,8 @@ BITNET_API int bitnet_fp4_linear(const void *x, int xdtype, int64_t ldx, const f
     if (M <= kFp4FusedTokens) {  // one launch
         Fp4SmallArgs a = fp4_small_args(w_scales, ga, gw, y, ydtype, M, N, K, ldy);
         a.x = x;
-        a.xtype = xdtype;
         a.ldx = ldx;
-        return launch_fp4_small(dev, nullptr, w, format, a, st);
+        return launch_fp4_small(dev, nullptr, xdtype, w, format, a, st);
     }
     uint8_t *codes = static_cast<uint8_t *>(workspace), *scales = codes + cb;
     if ((rc = launch_fp4_quant(x, xdtype, M, K, ldx, format, ga, codes, scales, st)) != BITNET_OK) return rc;

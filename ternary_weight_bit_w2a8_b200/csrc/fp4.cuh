@@ -51,23 +51,76 @@ struct Fp4Type<BITNET_FP32> {
     static __device__ __forceinline__ T from_f(float v) { return v; }
 };
 
-// 8 consecutive values of a row from column k, zeros from column K on.  `vec`:
-// every such group of the row starts on a 16-byte boundary.
+// 32 bytes of a row as they are stored: 16 values, or 8 of fp32.
 template <int DT>
-__device__ __forceinline__ void fp4_load8(const typename Fp4Type<DT>::T *__restrict__ row, int64_t k, int64_t K,
-                                          bool vec, float (&v)[8]) {
+struct Fp4Raw {
+    static constexpr int kValues = 32 / (int)sizeof(typename Fp4Type<DT>::T);
+    uint32_t w[8];
+};
+// From column k, zeros from column K on.  32 whole bytes in one load where
+// `wide` (they start on a 32-byte boundary), else two of 16 bytes; in any case
+// such a group starts on a 16-byte boundary.
+template <int DT>
+__device__ __forceinline__ Fp4Raw<DT> fp4_load32(const typename Fp4Type<DT>::T *__restrict__ row, int64_t k, int64_t K,
+                                                 bool wide) {
     using T = typename Fp4Type<DT>::T;
-    if (vec && k + 8 <= K) {
-        alignas(16) T t[8];
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(t) / 16; ++i)
-            reinterpret_cast<uint4 *>(t)[i] = __ldg(reinterpret_cast<const uint4 *>(row + k) + i);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = Fp4Type<DT>::to_f(t[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = k + i < K ? Fp4Type<DT>::to_f(row[k + i]) : 0.0f;
+    constexpr int kHalf = Fp4Raw<DT>::kValues / 2;
+    Fp4Raw<DT> v;
+    if (wide && k + 2 * kHalf <= K) {
+        asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]),
+                       "=r"(v.w[7])
+                     : "l"(row + k));
+        return v;
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int64_t c = k + i * kHalf;
+        if (c + kHalf <= K) {
+            reinterpret_cast<uint4 *>(v.w)[i] = __ldg(reinterpret_cast<const uint4 *>(row + c));
+        } else {
+            alignas(16) T t[kHalf];
+#pragma unroll
+            for (int j = 0; j < kHalf; ++j) t[j] = c + j < K ? row[c + j] : T(0.0f);
+            reinterpret_cast<uint4 *>(v.w)[i] = *reinterpret_cast<uint4 *>(t);
+        }
+    }
+    return v;
+}
+
+__device__ __forceinline__ uint32_t absmax2(uint32_t a, uint32_t b, __nv_bfloat16) {
+    const __nv_bfloat162 m = __hmax2_nan(__habs2(*reinterpret_cast<__nv_bfloat162 *>(&a)), *reinterpret_cast<__nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&m);
+}
+__device__ __forceinline__ uint32_t absmax2(uint32_t a, uint32_t b, __half) {
+    const __half2 m = __hmax2_nan(__habs2(*reinterpret_cast<__half2 *>(&a)), *reinterpret_cast<__half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&m);
+}
+
+// max |v| as fp32 bits: NaN, or infinity's bits, if one is among them.
+template <int DT>
+__device__ __forceinline__ uint32_t fp4_absmax(const Fp4Raw<DT> &v) {
+    uint32_t top = 0;
+    if constexpr (DT == BITNET_FP32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t b = v.w[i] & 0x7fffffffu;
+            top = b > top ? b : top;
+        }
+    } else {
+        using T = typename Fp4Type<DT>::T;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = absmax2(v.w[i], top, T(0.0f));
+        const uint16_t lo = (uint16_t)top, hi = (uint16_t)(top >> 16);  // magnitudes order as their bits do
+        const uint16_t m = lo > hi ? lo : hi;
+        top = __float_as_uint(Fp4Type<DT>::to_f(*reinterpret_cast<const T *>(&m))) & 0x7fffffffu;
+    }
+    return top;
+}
+
+template <int DT>
+__device__ __forceinline__ float fp4_value(const Fp4Raw<DT> &v, int i) {
+    return Fp4Type<DT>::to_f(reinterpret_cast<const typename Fp4Type<DT>::T *>(v.w)[i]);
 }
 
 // ------------------------------------------------------------------ rounding
@@ -107,20 +160,28 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
 // z / s rounded so that a comparison with any midpoint m of two e2m1 values
 // comes out as it does for the exact quotient.  s has four significant bits
 // and m three, so m s is an fp32 number: z is m s or at least one fp32 step
-// from it, which moves the quotient by more than half a step of m.  One
-// residual correction of z * r, r = fl32(1 / s), reaches that: the residual
-// z - q s is exact under fma, and q + residual * r is off by a step only
-// where the quotient is no midpoint.
+// from it, which moves the quotient by more than half a step of m (1.06 times
+// that at least).  One residual correction of z * r (Markstein 1990), r within
+// a step or two of 1 / s, reaches that: the residual z - q s is exact under
+// fma, and what r is off enters only through its product with the residual.
+// The same holds for top / 6 against the midpoints of e4m3 (five bits, 6 has
+// two).
 __device__ __forceinline__ float div_exact(float z, float s, float r) {
     const float q = __fmul_rn(z, r);
     return __fmaf_rn(__fmaf_rn(-q, s, z), r, q);
+}
+
+__device__ __forceinline__ float rcp_near(float s) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return r;
 }
 
 // Block scale from the bits of top = max |z| (an fp32 magnitude): its byte,
 // and what quantising divides by.
 struct Fp4Scale {
     uint32_t byte;
-    float s, r;  // NV: the scale and fl32(1 / scale) (0, 0 for a zero scale); MX: r = 1 / scale, exact
+    float s, r;  // NV: the scale and about 1 / scale (0, 0 for a zero scale); MX: r = 1 / scale, exact
 };
 
 template <int FMT>
@@ -135,10 +196,11 @@ __device__ __forceinline__ Fp4Scale fp4_scale(uint32_t top) {
         // 2^(127 - byte): byte <= 252, so never subnormal
         q.r = top >= 0x7f800000u ? 0.0f : __uint_as_float((254u - q.byte) << 23);
     } else {
-        q.byte = top >= 0x7f800000u ? 0x7fu : e4m3_bits(__fdiv_rn(__uint_as_float(top), 6.0f));
-        q.s = e4m3_value(q.byte);
-        q.r = q.s > 0.0f ? __frcp_rn(q.s) : 0.0f;
-        if (!(q.s > 0.0f)) q.s = 0.0f;
+        q.byte = top >= 0x7f800000u ? 0x7fu : e4m3_bits(div_exact(__uint_as_float(top), 6.0f, 0.16666667f));
+        const float s = e4m3_value(q.byte);
+        const bool some = s > 0.0f;  // neither zero nor NaN
+        q.s = some ? s : 0.0f;
+        q.r = some ? rcp_near(s) : 0.0f;
     }
     return q;
 }
@@ -154,54 +216,104 @@ __device__ __forceinline__ uint32_t fp4_codes8(const float (&z)[8], const Fp4Sca
 
 // ------------------------------------------------------------------ quantisation
 // A CTA quantises a patch of 128 rows x 256 k, so that it writes whole scale
-// tiles: a warp takes rows w, w + 8, ..., a lane 8 consecutive k of a row (one
-// 16-byte load of 16-bit values); the lanes of a block share its maximum by
-// shuffles; scale bytes are put together in shared memory.  The rows of the
+// tiles.  A lane takes 32 bytes of a row (16 values, 8 of fp32): one block of
+// NV, half of one of MX, or half and a quarter; the lanes of a block share its
+// maximum by shuffles.  A lane asks for four rows before it uses the first
+// (128 bytes in flight: 13824 x 5120 bf16 into NV takes 39 us, one row at a
+// time 53).  Scale bytes are put together in shared memory; the rows of the
 // last band past the matrix get scale 0.
+//   ALIGNED: rows of x start on 16-byte boundaries.  Otherwise a warp reads a
+// row's values in order, one to a lane, and shared memory turns them round.
 constexpr int kFp4PatchK = 256;
 
-template <int DT, int FMT>
+template <int DT, int FMT, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) fp4_quant_kernel(const typename Fp4Type<DT>::T *__restrict__ x,
                                                              int64_t rows, int64_t K, int64_t ldx,
                                                              const float *__restrict__ g, uint8_t *__restrict__ codes,
                                                              uint8_t *__restrict__ scales) {
+    using T = typename Fp4Type<DT>::T;
     constexpr int B = FMT == BITNET_FP4_MX ? 32 : 16;
+    constexpr int V = Fp4Raw<DT>::kValues;        // values of a lane
+    constexpr int kLanes = kFp4PatchK / V;        // lanes of a row: 16 or 32
     constexpr int kTiles = kFp4PatchK / (4 * B);  // scale tiles of a patch: 2 or 4
+    constexpr int kStep = kThreads / kLanes;      // rows that the CTA takes at once
+    constexpr int kAhead = ALIGNED ? 4 : 2;
     __shared__ alignas(16) uint8_t st[kTiles * kFp4TileBytes];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ alignas(16) T turn[ALIGNED ? 1 : kStep * kFp4PatchK];
+    const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
     const int64_t patches_k = ceil_div(k_pad(K), kFp4PatchK);
     const int64_t band = (int64_t)blockIdx.x / patches_k, pk = (int64_t)blockIdx.x % patches_k;
     const int64_t row_bytes = fp4_row_bytes(K), tiles = fp4_scale_tiles(K, FMT);
-    const int64_t k = pk * kFp4PatchK + 8 * lane;
-    const bool vec = ((reinterpret_cast<uintptr_t>(x) | (uintptr_t)(ldx * (int64_t)sizeof(*x))) & 15) == 0;
-    for (int i = threadIdx.x; i < kTiles * kFp4TileBytes / 4; i += kThreads) reinterpret_cast<uint32_t *>(st)[i] = 0;
+    const int64_t k = pk * kFp4PatchK + V * lane;
+    const bool wide = ((reinterpret_cast<uintptr_t>(x) | (uintptr_t)(ldx * (int64_t)sizeof(T))) & 31) == 0;
+    const int64_t left = rows - band * kFp4TileRows;
+    const int nrows = (int)(left < kFp4TileRows ? left : kFp4TileRows);
+    if (nrows < kFp4TileRows)
+        for (int i = threadIdx.x; i < kTiles * kFp4TileBytes / 4; i += kThreads) reinterpret_cast<uint32_t *>(st)[i] = 0;
     pdl_wait();
     pdl_launch_dependents();
     const float inv = g != nullptr ? __frcp_rn(*g) : 1.0f;
     __syncthreads();
-    const int64_t left = rows - band * kFp4TileRows;
-    const int nrows = (int)(left < kFp4TileRows ? left : kFp4TileRows);
-    const int tile = lane * 8 / (4 * B), col = (lane * 8 / B) & 3;
-    for (int r = warp; r < nrows; r += kThreads / 32) {
-        const int64_t row = band * kFp4TileRows + r;
-        float z[8];
-        fp4_load8<DT>(x + row * ldx, k, K, vec, z);
-        uint32_t top = 0;
+    x += band * kFp4TileRows * ldx;
+    codes += band * kFp4TileRows * row_bytes + k / 2;
+    const int at = (lane * V / (4 * B)) * kFp4TileBytes + (lane * V / B & 3);
+    const bool stored = k / 2 < row_bytes;
+    for (int r0 = group; r0 - group < nrows; r0 += kAhead * kStep) {  // (whole warps go on: they shuffle)
+        Fp4Raw<DT> v[kAhead];
+        if constexpr (ALIGNED) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            z[i] = __fmul_rn(z[i], inv);
-            const uint32_t b = __float_as_uint(z[i]) & 0x7fffffffu;
-            top = b > top ? b : top;
+            for (int i = 0; i < kAhead; ++i)
+                if (r0 + i * kStep < nrows) v[i] = fp4_load32<DT>(x + (r0 + i * kStep) * ldx, k, K, wide);
+        } else {
+            T t[kAhead][V];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const int64_t c = pk * kFp4PatchK + j * kLanes + lane;
+                    t[i][j] = r0 + i * kStep < nrows && c < K ? x[(r0 + i * kStep) * ldx + c] : T(0.0f);
+                }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < V; ++j) turn[group * kFp4PatchK + j * kLanes + lane] = t[i][j];
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    reinterpret_cast<uint4 *>(v[i].w)[j] =
+                        reinterpret_cast<const uint4 *>(turn + group * kFp4PatchK + V * lane)[j];
+            }
         }
 #pragma unroll
-        for (int o = 1; o < B / 8; o *= 2) {
-            const uint32_t t = __shfl_xor_sync(0xffffffffu, top, o);
-            top = t > top ? t : top;
+        for (int i = 0; i < kAhead; ++i) {
+            const int r = r0 + i * kStep;
+            // max |z| is fl32(max |x| * inv): rounding keeps order
+            uint32_t top = r < nrows ? fp4_absmax<DT>(v[i]) : 0u;
+            top = __float_as_uint(__fmul_rn(__uint_as_float(top), inv)) & 0x7fffffffu;
+#pragma unroll
+            for (int o = 1; o < B / V; o *= 2) {
+                const uint32_t t = __shfl_xor_sync(0xffffffffu, top, o);
+                top = t > top ? t : top;
+            }
+            if (r >= nrows) continue;
+            const Fp4Scale q = fp4_scale<FMT>(top);
+            uint32_t c[V / 8];
+#pragma unroll
+            for (int h = 0; h < V / 8; ++h) {
+                float z[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) z[j] = __fmul_rn(fp4_value<DT>(v[i], 8 * h + j), inv);
+                c[h] = fp4_codes8<FMT>(z, q, top < 0x7f800000u);
+            }
+            if (stored) {
+                if constexpr (V == 16)
+                    *reinterpret_cast<uint2 *>(codes + r * row_bytes) = make_uint2(c[0], c[1]);
+                else
+                    *reinterpret_cast<uint32_t *>(codes + r * row_bytes) = c[0];
+            }
+            if (lane % (B / V) == 0) st[at + 16 * (r & 31) + 4 * (r >> 5)] = (uint8_t)q.byte;
         }
-        const Fp4Scale q = fp4_scale<FMT>(top);
-        const uint32_t c = fp4_codes8<FMT>(z, q, top < 0x7f800000u);
-        if (k / 2 < row_bytes) *reinterpret_cast<uint32_t *>(codes + row * row_bytes + k / 2) = c;
-        if (lane % (B / 8) == 0) st[tile * kFp4TileBytes + 16 * (r & 31) + 4 * (r >> 5) + col] = (uint8_t)q.byte;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < kTiles * kFp4TileBytes / 16; i += kThreads) {
@@ -213,51 +325,114 @@ __global__ void __launch_bounds__(kThreads) fp4_quant_kernel(const typename Fp4T
 }
 
 // ------------------------------------------------------------------ reading back
-// y[r, k] = round(fl32(element * scale) * g); element * scale is exact.  A lane
-// takes 8 consecutive k of a row: 4 code bytes, one scale byte.
-template <int DT, int FMT>
+// y[r, k] = round(fl32(element * scale) * g); element * scale is exact.
+
+// The value of a code: its three magnitude bits as exponent and mantissa of an
+// fp32 number stand for the e2m1 value times 2^-126 (subnormals included).
+__device__ __forceinline__ float e2m1_value(uint32_t code) {
+    const float e = __uint_as_float((code & 7u) << 22) * 8.507059173023462e37f;  // 2^126
+    return __uint_as_float(__float_as_uint(e) | ((code & 8u) << 28));
+}
+
+// A CTA reads a patch of 128 rows x 256 k; a lane takes 32 bytes of a row of y
+// (16 values from 8 code bytes, 8 of fp32 from 4).  ALIGNED (rows of y start on
+// 16-byte boundaries): stored as they are, at once where they start on a
+// 32-byte boundary.  Otherwise the lanes of a row put them down in shared
+// memory as 4-byte words that lie on 4-byte boundaries of y (shifted by one
+// value where the row starts between two) and store those in order: 997 x 6910
+// fp16 took 22 us with lanes that stored their own pairs.
+template <int DT, int FMT, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) fp4_dequant_kernel(const uint8_t *__restrict__ codes,
                                                                const uint8_t *__restrict__ scales, int64_t rows,
                                                                int64_t K, const float *__restrict__ g,
                                                                typename Fp4Type<DT>::T *__restrict__ y, int64_t ldy) {
     using T = typename Fp4Type<DT>::T;
     constexpr int B = FMT == BITNET_FP4_MX ? 32 : 16;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int V = Fp4Raw<DT>::kValues, kLanes = kFp4PatchK / V, kStep = kThreads / kLanes, kAhead = 4;
+    constexpr int kRowWords = 8 * kLanes + kLanes;  // a word of padding after 8: lanes 8 words apart share no banks
+    __shared__ uint32_t turn[ALIGNED ? 1 : kStep * kRowWords];
     const int64_t patches_k = ceil_div(k_pad(K), kFp4PatchK);
     const int64_t band = (int64_t)blockIdx.x / patches_k, pk = (int64_t)blockIdx.x % patches_k;
-    const int64_t row_bytes = fp4_row_bytes(K), tiles = fp4_scale_tiles(K, FMT);
-    const int64_t k = pk * kFp4PatchK + 8 * lane;
-    const bool vec = ((reinterpret_cast<uintptr_t>(y) | (uintptr_t)(ldy * (int64_t)sizeof(T))) & 15) == 0;
-    pdl_wait();
-    pdl_launch_dependents();
-    if (k >= K) return;
-    const float gs = g != nullptr ? *g : 1.0f;
+    const int64_t row_bytes = fp4_row_bytes(K), tiles = fp4_scale_tiles(K, FMT), k0 = pk * kFp4PatchK;
     const int64_t left = rows - band * kFp4TileRows;
     const int nrows = (int)(left < kFp4TileRows ? left : kFp4TileRows);
-    const uint8_t *sp = scales + (band * tiles + k / (4 * B)) * kFp4TileBytes + (k / B & 3);
-    for (int r = warp; r < nrows; r += kThreads / 32) {
-        const int64_t row = band * kFp4TileRows + r;
-        const uint32_t c = *reinterpret_cast<const uint32_t *>(codes + row * row_bytes + k / 2);
-        const uint32_t sb = sp[16 * (r & 31) + 4 * (r >> 5)];
-        const float s = FMT == BITNET_FP4_MX ? e8m0_value(sb) : e4m3_value(sb);
-        alignas(16) T t[8];
+    const bool wide = ((reinterpret_cast<uintptr_t>(y) | (uintptr_t)(ldy * (int64_t)sizeof(T))) & 31) == 0;
+    const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes, k = V * lane;
+    pdl_wait();
+    pdl_launch_dependents();
+    const float gs = g != nullptr ? *g : 1.0f;
+    codes += band * kFp4TileRows * row_bytes + (k0 + k) / 2;
+    scales += (band * tiles + (k0 + k) / (4 * B)) * kFp4TileBytes + (k / B & 3);
+    y += band * kFp4TileRows * ldy + k0;
+    const int cols = (int)(K - k0 < kFp4PatchK ? K - k0 : kFp4PatchK);
+    uint32_t *words = turn + group * kRowWords;
+    for (int r0 = group; r0 - group < nrows; r0 += kAhead * kStep) {  // (whole warps go on: they shuffle)
+        uint32_t c[kAhead][V / 8], sb[kAhead];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            // the three magnitude bits as exponent and mantissa of an fp32
-            // number stand for the e2m1 value times 2^-126 (subnormals included)
-            const uint32_t n = c >> (4 * i);
-            const float e = __uint_as_float((n & 7u) << 22) * 8.507059173023462e37f;  // 2^126
-            const float v = __uint_as_float(__float_as_uint(e) | ((n & 8u) << 28));
-            t[i] = Fp4Type<DT>::from_f(__fmul_rn(__fmul_rn(v, s), gs));
+        for (int i = 0; i < kAhead; ++i) {
+            const int r = r0 + i * kStep;
+            if (r < nrows && k < cols) {
+#pragma unroll
+                for (int h = 0; h < V / 8; ++h)
+                    c[i][h] = *reinterpret_cast<const uint32_t *>(codes + r * row_bytes + 4 * h);
+                sb[i] = scales[16 * (r & 31) + 4 * (r >> 5)];
+            }
         }
-        T *yp = y + row * ldy + k;
-        if (vec && k + 8 <= K) {
 #pragma unroll
-            for (int i = 0; i < (int)sizeof(t) / 16; ++i) reinterpret_cast<uint4 *>(yp)[i] = reinterpret_cast<uint4 *>(t)[i];
-        } else {
+        for (int i = 0; i < kAhead; ++i) {
+            const int r = r0 + i * kStep;
+            if (ALIGNED && (r >= nrows || k >= cols)) continue;
+            const float s = FMT == BITNET_FP4_MX ? e8m0_value(sb[i]) : e4m3_value(sb[i]);
+            alignas(16) T t[V];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (k + i < K) yp[i] = t[i];
+            for (int j = 0; j < V; ++j)
+                t[j] = Fp4Type<DT>::from_f(__fmul_rn(__fmul_rn(e2m1_value(c[i][j / 8] >> (4 * (j & 7))), s), gs));
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(t);
+            T *yr = y + r * ldy;
+            if constexpr (ALIGNED) {
+                if (wide && k + V <= cols) {
+                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(yr + k), "r"(w[0]),
+                                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                                 : "memory");
+                    continue;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (k + (h + 1) * (V / 2) <= cols) {
+                        reinterpret_cast<uint4 *>(yr + k)[h] = reinterpret_cast<const uint4 *>(t)[h];
+                    } else {
+#pragma unroll
+                        for (int j = h * (V / 2); j < (h + 1) * (V / 2); ++j)
+                            if (k + j < cols) yr[k + j] = t[j];
+                    }
+                }
+            } else {
+                constexpr int kPer = 4 / (int)sizeof(T);  // values of a word
+                // word q holds values kPer q - odd and the next
+                const int odd = kPer == 2 ? (int)(reinterpret_cast<uintptr_t>(yr) >> 1 & 1) : 0;
+                const uint32_t before = __shfl_up_sync(0xffffffffu, w[7], 1);
+                __syncwarp();  // the words of the row before have been read
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    words[9 * lane + j] = odd ? __funnelshift_l(j > 0 ? w[j > 0 ? j - 1 : 0] : before, w[j], 16) : w[j];
+                __syncwarp();
+                if (r < nrows) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int q = lane + j * kLanes, e = kPer * q - odd;
+                        const uint32_t v = words[q + (q >> 3)];
+                        if (e >= 0 && e + kPer <= cols) {
+                            *reinterpret_cast<uint32_t *>(yr + e) = v;
+                        } else if (kPer == 2) {  // the row's first or last value alone
+                            const uint16_t half = (uint16_t)(e < 0 ? v >> 16 : v);
+                            const int at = e < 0 ? 0 : e;
+                            if (at < cols) yr[at] = *reinterpret_cast<const T *>(&half);
+                        }
+                    }
+                    // the patch's last value, where the words end one before it
+                    if (odd && lane == kLanes - 1 && cols == kFp4PatchK) yr[kFp4PatchK - 1] = t[V - 1];
+                }
+            }
         }
     }
 }
@@ -265,45 +440,78 @@ __global__ void __launch_bounds__(kThreads) fp4_dequant_kernel(const uint8_t *__
 // ------------------------------------------------------------------ tensor scale
 // g = max(fl32(max |x| / 2688), 2^-126) over the finite values of x (2688 =
 // 6 * 448: the largest value the NV format holds at g = 1; the lower end keeps
-// 1 / g finite).  Two launches: a maximum per CTA, then one CTA over those;
-// maxima do not depend on any order.
-constexpr int kFp4ScaleMaxBlocks = 1184;
+// 1 / g finite).  Rounding keeps order, so g is also the largest of the CTAs'
+// own values: they meet in an atomic maximum of the bits (positive floats order
+// as their bits do; a maximum does not depend on the order), g having been set
+// to 0 by a launch before; one CTA alone stores it.  A warp takes a piece of a
+// row at a time, eight 32-byte loads to a lane; the values before the row's
+// first 32-byte boundary and behind its last are taken one by one.
+__global__ void fp4_clear_kernel(float *g) {
+    pdl_wait();
+    pdl_launch_dependents();
+    *g = 0.0f;
+}
+
+constexpr int kFp4ScaleLoads = 8;
+template <int DT>
+constexpr int kFp4ScalePiece = Fp4Raw<DT>::kValues * 32 * kFp4ScaleLoads;
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads) fp4_absmax_kernel(const typename Fp4Type<DT>::T *__restrict__ x,
-                                                              int64_t rows, int64_t K, int64_t ldx,
-                                                              uint32_t *__restrict__ partial) {
+__global__ void __launch_bounds__(kThreads) fp4_tensor_scale_kernel(const typename Fp4Type<DT>::T *__restrict__ x,
+                                                                    int64_t rows, int64_t K, int64_t ldx, float *g) {
+    using T = typename Fp4Type<DT>::T;
+    constexpr int V = Fp4Raw<DT>::kValues;
     __shared__ uint32_t red[32];
-    const bool vec = ((reinterpret_cast<uintptr_t>(x) | (uintptr_t)(ldx * (int64_t)sizeof(*x))) & 15) == 0;
-    const int64_t per_row = ceil_div(K, 8), total = rows * per_row;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t per_row = ceil_div(K, kFp4ScalePiece<DT>), total = rows * per_row;
     pdl_wait();
     pdl_launch_dependents();
     uint32_t top = 0;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
-        const int64_t row = i / per_row;
-        float v[8];
-        fp4_load8<DT>(x + row * ldx, 8 * (i - row * per_row), K, vec, v);
+    auto one = [&](T v) {
+        const uint32_t b = __float_as_uint(Fp4Type<DT>::to_f(v)) & 0x7fffffffu;
+        top = b < 0x7f800000u && b > top ? b : top;
+    };
+    for (int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + warp; i < total; i += (int64_t)gridDim.x * (kThreads / 32)) {
+        const int64_t row = i / per_row, piece = i - row * per_row;
+        const T *xr = x + row * ldx;
+        int64_t head = (int64_t)((0 - reinterpret_cast<uintptr_t>(xr)) & 31) / (int64_t)sizeof(T);
+        if (head > K) head = K;
+        const int64_t end = head + (K - head) / V * V;  // of the whole 32-byte groups
+        const int64_t k0 = head + piece * kFp4ScalePiece<DT> + V * lane;
+        Fp4Raw<DT> v[kFp4ScaleLoads];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t b = __float_as_uint(v[j]) & 0x7fffffffu;
-            top = b < 0x7f800000u && b > top ? b : top;
+        for (int j = 0; j < kFp4ScaleLoads; ++j) {
+            const int64_t k = k0 + j * 32 * V;
+            if (k < end) {
+                v[j] = fp4_load32<DT>(xr, k, K, true);
+            } else {
+#pragma unroll
+                for (int w = 0; w < 8; ++w) v[j].w[w] = 0;
+            }
+        }
+        if (piece == 0) {
+            if (lane < head) one(xr[lane]);
+            if (end + lane < K) one(xr[end + lane]);
+        }
+#pragma unroll
+        for (int j = 0; j < kFp4ScaleLoads; ++j) {
+            const uint32_t t = fp4_absmax<DT>(v[j]);
+            if (t < 0x7f800000u) {
+                top = t > top ? t : top;
+            } else {  // the finite ones among them
+#pragma unroll
+                for (int e = 0; e < V; ++e) one(reinterpret_cast<const T *>(v[j].w)[e]);
+            }
         }
     }
     top = block_reduce(top, [](uint32_t a, uint32_t b) { return a > b ? a : b; }, red);
-    if (threadIdx.x == 0) partial[blockIdx.x] = top;
-}
-
-__global__ void __launch_bounds__(kThreads) fp4_tensor_scale_kernel(const uint32_t *__restrict__ partial, int n,
-                                                                    float *__restrict__ g) {
-    __shared__ uint32_t red[32];
-    pdl_wait();
-    pdl_launch_dependents();
-    uint32_t top = 0;
-    for (int i = threadIdx.x; i < n; i += kThreads) top = partial[i] > top ? partial[i] : top;
-    top = block_reduce(top, [](uint32_t a, uint32_t b) { return a > b ? a : b; }, red);
     if (threadIdx.x == 0) {
         const float v = __fdiv_rn(__uint_as_float(top), 2688.0f);
-        *g = v > 1.17549435e-38f ? v : 1.17549435e-38f;
+        const float s = v > 1.17549435e-38f ? v : 1.17549435e-38f;
+        if (gridDim.x == 1)
+            *g = s;
+        else
+            atomicMax(reinterpret_cast<uint32_t *>(g), __float_as_uint(s));
     }
 }
 

@@ -94,14 +94,14 @@ __device__ __forceinline__ void fp4_store(void *y, int64_t i, float v, int dtype
 }
 
 // ------------------------------------------------------------------ few tokens
-// Up to 128 tokens: reading the weights bounds the call.  The weights are the
+// Up to 64 tokens: reading the weights bounds the call.  The weights are the
 // MMA's row operand (128 rows of them a tile), the tokens its BT columns, so
 // that one pass over the weights serves all tokens.  Tiles are few (20 for
 // 2560 rows), so a cluster of up to 8 CTAs shares a tile, each with a range of
 // k; the CTAs add their fp32 sums up through distributed shared memory, in
 // rank order, each for its share of the rows.  No workspace, no atomics, and
-// the same bits every time.  Two CTAs fit an SM, so that one's start and end
-// overlap the other's loads.
+// the same bits every time.  Three CTAs fit an SM (two from 17 tokens up), so
+// that one's start and end overlap the others' loads.
 //   Before the launch-chain wait the first boxes of the weights are only asked
 // into L2: what an earlier kernel still writes is read after the wait.
 //   QX: up to 16 tokens of x are quantised by the epilogue warps stage by
@@ -111,7 +111,7 @@ struct Fp4SmallArgs {
     const uint8_t *sw, *sa;  // scale tiles of the weights and of the tokens
     const void *x;           // QX: the tokens [M, K], row stride ldx
     int64_t ldx;
-    int xtype, ytype;
+    int ytype;
     int M;
     int64_t N, K, ldy;
     const float *ga, *gw;
@@ -124,15 +124,17 @@ struct Fp4Small {
     static constexpr int kTiles = FMT == BITNET_FP4_MX ? 2 : 4;  // scale tiles per stage and 128 rows
     static constexpr int kPBytes = kFp4Rows * 128, kQBytes = BT * 128, kS = kTiles * kFp4TileBytes;
     static constexpr int kStage = kPBytes + kQBytes + 2 * kS;
-    static constexpr int kStages = 110 * 1024 / kStage < 6 ? 110 * 1024 / kStage : 6;
+    static constexpr int kCtas = BT <= 16 ? 3 : 2;               // CTAs per SM
+    static constexpr int kStages = (kCtas == 3 ? 73 : 111) * 1024 / kStage;
     static constexpr int kBars = kStages * kStage;
     static constexpr int kBytes = kBars + (2 * kStages + 2) * 8 + 16;
     static constexpr int kSlotCols = 8 * kTiles;                 // tensor-memory columns of a stage's scales
-    static constexpr int kNeed = BT + 2 * kSlotCols;
+    static constexpr int kNeed = BT + kStages * kSlotCols;
     static constexpr int kCols = kNeed <= 32 ? 32 : kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : 256;
-    static_assert(kNeed <= 256 && kStages >= 3 && BT % 16 == 0 && BT <= 128, "tile");
+    static_assert(kNeed <= 256 && kCtas * kCols <= 512 && kStages >= 3 && BT % 16 == 0 && BT <= 64, "tile");
     static_assert(kStage % 1024 == 0 && kQBytes % 1024 == 0, "swizzled rows");
     static_assert(kFp4Rows * BT * 4 <= kBars, "partial sums take the stages' place");
+    static_assert(BT >= 16, "accumulators are read 16 columns at a time");
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -150,9 +152,12 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
@@ -162,28 +167,100 @@ __device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int x, i
     asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
 }
 
-// 8 values of row m from column k for the quantiser warps.
-__device__ __forceinline__ void fp4_load8_any(const Fp4SmallArgs &a, int m, int64_t k, float (&v)[8]) {
-    if (a.xtype == BITNET_FP32) {
-        const float *r = static_cast<const float *>(a.x) + m * a.ldx;
-        fp4_load8<BITNET_FP32>(r, k, a.K, (reinterpret_cast<uintptr_t>(r) & 15) == 0, v);
-    } else if (a.xtype == BITNET_FP16) {
-        const __half *r = static_cast<const __half *>(a.x) + m * a.ldx;
-        fp4_load8<BITNET_FP16>(r, k, a.K, (reinterpret_cast<uintptr_t>(r) & 15) == 0, v);
-    } else {
-        const __nv_bfloat16 *r = static_cast<const __nv_bfloat16 *>(a.x) + m * a.ldx;
-        fp4_load8<BITNET_BF16>(r, k, a.K, (reinterpret_cast<uintptr_t>(r) & 15) == 0, v);
+constexpr int kFp4Quantised = -1;  // XT: the tokens come quantised
+
+// The quantiser warps of the small kernel: warp w of four.  As in
+// fp4_quant_kernel a lane takes 32 bytes of a token; so a warp takes two tokens
+// at a time (one of fp32), and its tokens of a stage are w RW, w RW + 1, ...,
+// then 4 RW further.  The next stage's values are on their way while this one's
+// are quantised.
+template <int FMT, int BT, int XT>
+__device__ __forceinline__ void fp4_quantise_stages(const Fp4SmallArgs &a, uint8_t *sm, uint64_t *full, uint64_t *empty,
+                                                    int i0, int n_i, int w, int warp_lane, volatile int *abort_flag) {
+    using L = Fp4Small<FMT, BT>;
+    using T = typename Fp4Type<XT>::T;
+    constexpr int S = L::kStages, B = FMT == BITNET_FP4_MX ? 32 : 16;
+    constexpr int V = Fp4Raw<XT>::kValues, kLanes = kFp4StageK / V, RW = 32 / kLanes;
+    constexpr int kTurns = kFp4FusedTokens / (4 * RW);
+    const int lane = warp_lane % kLanes, m0 = w * RW + warp_lane / kLanes;
+    const T *x = static_cast<const T *>(a.x);
+    const uintptr_t where = reinterpret_cast<uintptr_t>(x) | (uintptr_t)(a.ldx * (int64_t)sizeof(T));
+    const float inv = a.ga != nullptr ? __frcp_rn(*a.ga) : 1.0f;
+    Fp4Raw<XT> next[kTurns];
+    auto load = [&](int i) {
+        const int64_t k = (int64_t)(i0 + i) * kFp4StageK + V * lane;
+#pragma unroll
+        for (int t = 0; t < kTurns; ++t) {
+            const int m = m0 + 4 * RW * t;
+            if (m >= a.M) continue;
+            if ((where & 15) == 0) {
+                next[t] = fp4_load32<XT>(x + m * a.ldx, k, a.K, (where & 31) == 0);
+            } else {
+                alignas(16) T v[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[e] = k + e < a.K ? x[m * a.ldx + k + e] : T(0.0f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) next[t].w[e] = reinterpret_cast<const uint32_t *>(v)[e];
+            }
+        }
+    };
+    load(0);
+    int s = 0;
+    uint32_t phase = 1;  // of `empty`: passes at once in the first round
+    for (int i = 0; i < n_i; ++i) {
+        // the lanes stop together (they shuffle below)
+        if (!warp_wait(&empty[s], phase, abort_flag)) break;
+        uint8_t *q = sm + s * L::kStage + L::kPBytes, *sq = q + L::kQBytes + L::kS;
+        Fp4Raw<XT> v[kTurns];
+#pragma unroll
+        for (int t = 0; t < kTurns; ++t) v[t] = next[t];
+        if (i + 1 < n_i) load(i + 1);
+#pragma unroll
+        for (int t = 0; t < kTurns; ++t) {
+            const int m = m0 + 4 * RW * t;
+            if (m - warp_lane / kLanes >= a.M) break;  // (both tokens of the warp)
+            uint32_t top = m < a.M ? fp4_absmax<XT>(v[t]) : 0u;
+            top = __float_as_uint(__fmul_rn(__uint_as_float(top), inv)) & 0x7fffffffu;
+#pragma unroll
+            for (int o = 1; o < B / V; o *= 2) {
+                const uint32_t u = __shfl_xor_sync(0xffffffffu, top, o);
+                top = u > top ? u : top;
+            }
+            if (m >= a.M) continue;
+            const Fp4Scale sc = fp4_scale<FMT>(top);
+            uint32_t c[V / 8];
+#pragma unroll
+            for (int h = 0; h < V / 8; ++h) {
+                float z[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) z[e] = __fmul_rn(fp4_value<XT>(v[t], 8 * h + e), inv);
+                c[h] = fp4_codes8<FMT>(z, sc, top < 0x7f800000u);
+            }
+            // 16-byte piece p of token m lies at piece p ^ (m % 8) of its row
+            const int byte = V / 2 * lane;
+            uint8_t *to = q + m * 128 + ((((byte >> 4) ^ m) & 7) << 4) + (byte & 15);
+            if constexpr (V == 16)
+                *reinterpret_cast<uint2 *>(to) = make_uint2(c[0], c[1]);
+            else
+                *reinterpret_cast<uint32_t *>(to) = c[0];
+            if (lane % (B / V) == 0) sq[(lane * V / (4 * B)) * kFp4TileBytes + 16 * m + (lane * V / B & 3)] = (uint8_t)sc.byte;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (warp_lane == 0) mbar_arrive(&full[s]);
+        if (++s == S) s = 0, phase ^= 1;
     }
+    __syncwarp();
 }
 
-template <int FMT, int BT, bool QX>
-__global__ void __launch_bounds__(kFp4Threads, 2)
+template <int FMT, int BT, int XT>
+__global__ void __launch_bounds__(kFp4Threads, Fp4Small<FMT, BT>::kCtas)
     fp4_small_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap,
                      const Fp4SmallArgs a) {
     using L = Fp4Small<FMT, BT>;
+    constexpr bool QX = XT != kFp4Quantised;
     static_assert(!QX || BT >= kFp4FusedTokens, "fused tokens");
     constexpr int S = L::kStages;
-    constexpr int B = FMT == BITNET_FP4_MX ? 32 : 16;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + L::kBars);
@@ -267,99 +344,49 @@ __global__ void __launch_bounds__(kFp4Threads, 2)
         // wait is bounded)
         for (int j = i - S < 0 ? 0 : i - S; j < i; ++j) mbar_wait_bounded(&full[j % S], (uint32_t)(j / S) & 1u);
     } else if (warp == 1) {
-        constexpr uint32_t idesc = fp4_idesc(FMT, kFp4Rows, BT);
-        bool ok = true;
-        for (int i = 0; i < n_i; ++i) {
-            const int s = i % S;
-            // two sets of scale columns take turns: the MMAs that read this
-            // one, two stages ago, are done
-            ok = warp_wait(&full[s], (uint32_t)(i / S) & 1u, abort_flag) &&
-                 (i < 2 || warp_wait(&empty[(i - 2) % S], (uint32_t)((i - 2) / S) & 1u, abort_flag));
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-                const uint32_t pa = smem_u32(sm + s * L::kStage), qa = pa + L::kPBytes;
-                const uint32_t spa = qa + L::kQBytes, sqa = spa + L::kS;
-                const uint32_t cp = tmem + (uint32_t)(BT + (i & 1) * L::kSlotCols), cq = cp + 4 * L::kTiles;
-                const int64_t left = (kp - (int64_t)(i0 + i) * kFp4StageK) / 64;
-                const int steps = (int)(left < 4 ? left : 4);
+        if (elect_one()) {
+            constexpr uint32_t idesc = fp4_idesc(FMT, kFp4Rows, BT);
+            const uint32_t base = smem_u32(sm);
+            const uint64_t w0 = umma_desc_sw128(base), a0 = umma_desc_sw128(base + L::kPBytes);
+            const uint64_t s0 = scale_desc(base + L::kPBytes + L::kQBytes);
+            const int full_stages = (int)(kp / kFp4StageK) - i0;  // the last stage may hold 128 k only
+            bool ok = true;
+            int s = 0;
+            uint32_t phase = 0;
+            for (int i = 0; i < n_i; ++i) {
+                if (!tc_wait(&full[s], phase, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t at = (uint64_t)(s * (L::kStage >> 4));
+                const uint32_t cw = tmem + (uint32_t)(BT + s * L::kSlotCols), ca = cw + 4 * L::kTiles;
+                const bool whole = i < full_stages;
 #pragma unroll
                 for (int t = 0; t < L::kTiles; ++t) {
-                    tmem_cp_scales(cp + 4 * t, scale_desc(spa + t * kFp4TileBytes));
-                    tmem_cp_scales(cq + 4 * t, scale_desc(sqa + t * kFp4TileBytes));
+                    if (t < L::kTiles / 2 || whole) {
+                        tmem_cp_scales(cw + 4 * t, s0 + at + (uint64_t)(t * kFp4TileBytes >> 4));
+                        tmem_cp_scales(ca + 4 * t, s0 + at + (uint64_t)((L::kS + t * kFp4TileBytes) >> 4));
+                    }
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (j < steps) {
-                        const int t = FMT == BITNET_FP4_MX ? j >> 1 : j;
-                        const int id = FMT == BITNET_FP4_MX ? (j & 1) * 2 : 0;
-                        umma_fp4<FMT>(tmem, umma_desc_sw128(pa + 32 * j), umma_desc_sw128(qa + 32 * j),
-                                      idesc | fp4_scale_id(id), cp + 4 * t, cq + 4 * t, (i > 0 || j > 0) ? 1u : 0u);
-                    }
+                    const int t = FMT == BITNET_FP4_MX ? j >> 1 : j;
+                    const int id = FMT == BITNET_FP4_MX ? (j & 1) * 2 : 0;
+                    if (j < 2 || whole)
+                        umma_fp4<FMT>(tmem, w0 + at + 2 * j, a0 + at + 2 * j, idesc | fp4_scale_id(id), cw + 4 * t,
+                                      ca + 4 * t, j > 0 ? 1u : (uint32_t)(i > 0));
                 }
                 umma_commit(&empty[s]);
+                if (++s == S) s = 0, phase ^= 1;
             }
-            __syncwarp();
+            umma_commit(ok ? done : drain);
+            // on an abort the MMAs issued so far end before tensor memory is freed
+            if (!ok) mbar_wait_bounded(drain, 0);
         }
-        if (elect_one()) umma_commit(ok ? done : drain);
         __syncwarp();
-        // on an abort the MMAs issued so far end before tensor memory is freed
-        if (!ok) mbar_wait_bounded(drain, 0);
     } else {
-        if (QX) {
-            // warp w of four takes tokens w, w + 4, ...; a lane 8 of a stage's 256 k.  The next stage's values are
-            // on their way while this one's are quantised.
-            const int w = warp - 2;
-            constexpr int R = kFp4FusedTokens / 4;
-            const float inv = a.ga != nullptr ? __frcp_rn(*a.ga) : 1.0f;
-            float z[R][8];
-            auto load = [&](int i) {
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-                    if (w + 4 * r < a.M) fp4_load8_any(a, w + 4 * r, (int64_t)(i0 + i) * kFp4StageK + 8 * lane, z[r]);
-            };
-            load(0);
-            for (int i = 0; i < n_i; ++i) {
-                const int s = i % S;
-                // the lanes stop together (they shuffle below)
-                if (i >= S && !warp_wait(&empty[s], (uint32_t)(i / S - 1) & 1u, abort_flag)) break;
-                uint8_t *q = sm + s * L::kStage + L::kPBytes, *sq = q + L::kQBytes + L::kS;
-                float v[R][8];
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[r][e] = z[r][e];
-                if (i + 1 < n_i) load(i + 1);
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const int m = w + 4 * r;
-                    if (m < a.M) {
-                        uint32_t top = 0;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            v[r][e] = __fmul_rn(v[r][e], inv);
-                            const uint32_t b = __float_as_uint(v[r][e]) & 0x7fffffffu;
-                            top = b > top ? b : top;
-                        }
-#pragma unroll
-                        for (int o = 1; o < B / 8; o *= 2) {
-                            const uint32_t t = __shfl_xor_sync(0xffffffffu, top, o);
-                            top = t > top ? t : top;
-                        }
-                        const Fp4Scale sc = fp4_scale<FMT>(top);
-                        // 16-byte chunk c of row m lies at chunk c ^ (m % 8)
-                        *reinterpret_cast<uint32_t *>(q + m * 128 + ((((lane >> 2) ^ m) & 7) << 4) + 4 * (lane & 3)) =
-                            fp4_codes8<FMT>(v[r], sc, top < 0x7f800000u);
-                        if (lane % (B / 8) == 0)
-                            sq[(lane * 8 / (4 * B)) * kFp4TileBytes + 16 * m + ((lane * 8 / B) & 3)] = (uint8_t)sc.byte;
-                    }
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[s]);
-            }
-            __syncwarp();
-        }
+        if constexpr (QX) fp4_quantise_stages<FMT, BT, XT>(a, sm, full, empty, i0, n_i, warp - 2, lane, abort_flag);
         const int quarter = warp & 3;
         const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16);
         const int row = quarter * 32 + lane;
@@ -388,19 +415,23 @@ __global__ void __launch_bounds__(kFp4Threads, 2)
     if (a.split > 1) {
         cluster_sync();  // every CTA's sums are in its shared memory
         const float g = (a.ga != nullptr ? *a.ga : 1.0f) * (a.gw != nullptr ? *a.gw : 1.0f);
-        const int rows = kFp4Rows / a.split, r0 = rank * rows;
+        // four neighbouring rows of a token at a time: one 16-byte read of each CTA's sums
+        const int quads = kFp4Rows / 4 / a.split, r0 = rank * (kFp4Rows / a.split);
         const uint32_t base = smem_u32(sm);
-        for (int e = threadIdx.x; e < a.M * rows; e += kFp4Threads) {
-            const int c = e / rows, row = r0 + e % rows;
+        for (int e = threadIdx.x; e < a.M * quads; e += kFp4Threads) {
+            const int c = e / quads, row = r0 + 4 * (e % quads);
             const int64_t n = (int64_t)tile * kFp4Rows + row;
             const uint32_t at = base + (uint32_t)(c * kFp4Rows + row) * 4;
-            float v[kFp4MaxSplit];
+            float4 v[kFp4MaxSplit];
 #pragma unroll
-            for (int r = 0; r < kFp4MaxSplit; ++r) v[r] = r < a.split ? ld_cluster(map_rank(at, (uint32_t)r)) : 0.0f;
-            float sum = v[0];
+            for (int r = 0; r < kFp4MaxSplit; ++r)
+                v[r] = r < a.split ? ld_cluster_v4(map_rank(at, (uint32_t)r)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int r = 1; r < kFp4MaxSplit; ++r) sum += v[r];
-            if (n < a.N) fp4_store(a.y, c * a.ldy + n, __fmul_rn(sum, g), a.ytype);
+            for (int r = 1; r < kFp4MaxSplit; ++r) v[0].x += v[r].x, v[0].y += v[r].y, v[0].z += v[r].z, v[0].w += v[r].w;
+            const float o[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (n + i < a.N) fp4_store(a.y, c * a.ldy + n + i, __fmul_rn(o[i], g), a.ytype);
         }
         cluster_sync();  // nobody reads this CTA's shared memory any more
     } else {

@@ -354,11 +354,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
                         }
                     }
                 } else {
-                    for (int r = 0; r < rows; ++r)
-                        for (int e = lane; e < 8 * pieces; e += 32)
-                            if (nb + e < a.N)
-                                y[r * a.ldy + nb + e] =
-                                    *reinterpret_cast<const uint16_t *>(box + r * 128 + (((e >> 3) ^ (r & 7)) << 4) + 2 * (e & 7));
+                    // A lane stores the pair of a row's values that lies on a 4-byte boundary of y; where the row starts
+                    // between two, the last lane has the box's last value and its first.  Eight rows are read before
+                    // the first is stored (one by one, a store holds up the next row's reads).
+                    const int width = 8 * pieces, last = width / 2 - 1;
+                    const int cols = (int)(a.N - nb < width ? a.N - nb : width);
+                    auto value = [&](int r, int e) -> uint32_t {
+                        return *reinterpret_cast<const uint16_t *>(box + r * 128 + (((e >> 3) ^ (r & 7)) << 4) + 2 * (e & 7));
+                    };
+                    const uintptr_t y0 = reinterpret_cast<uintptr_t>(y + nb);
+                    for (int r0 = 0; r0 < rows && lane <= last; r0 += 8) {
+                        uint32_t pr[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int e = 2 * lane + (int)((y0 >> 1) + (r0 + i) * a.ldy & 1);
+                            pr[i] = value(r0 + i, e) | value(r0 + i, (e + 1) & (width - 1)) << 16;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if (r0 + i >= rows) break;
+                            uint16_t *yr = y + (r0 + i) * a.ldy + nb;
+                            const int odd = (int)((y0 >> 1) + (r0 + i) * a.ldy & 1), e = 2 * lane + odd;
+                            if (e + 1 < cols)
+                                *reinterpret_cast<uint32_t *>(yr + e) = pr[i];
+                            else if (e < cols)
+                                yr[e] = (uint16_t)pr[i];
+                            if (odd && lane == last && cols > 0) yr[0] = (uint16_t)(pr[i] >> 16);
+                        }
+                    }
                 }
             }
         }

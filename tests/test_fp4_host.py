@@ -32,6 +32,7 @@ def test_sizes(lib):
         for fmt in (ref.MX, ref.NV):
             assert bn.bitnet_fp4_scale_bytes(rows, K, fmt) == ref.pad_up(rows, 128) * Kp // ref.BLOCK[fmt]
             ws = bn.bitnet_fp4_workspace_bytes(rows, 64, K, fmt)
+            assert bn.bitnet_fp4_workspace_bytes(16, 64, K, fmt) == 0
             if rows > 16:  # the linear layer's codes and scales
                 assert ws >= rows * Kp // 2 + ref.pad_up(rows, 128) * Kp // ref.BLOCK[fmt]
             assert ws == bn.bitnet_fp4_workspace_bytes(rows, 64, K, fmt)
@@ -83,14 +84,12 @@ def test_dequant_refusals(no_gpu):
 
 def test_tensor_scale_refusals(no_gpu):
     f = no_gpu.bitnet_fp4_tensor_scale
-    need = bn.bitnet_fp4_workspace_bytes(4, 1, 64, 1)
-    assert f(A, 0, 4, 64, 64, NULL, WS, need, S) == INV
-    assert f(A, 7, 4, 64, 64, A, WS, need, S) == INV
-    assert f(A, 0, 4, 64, 60, A, WS, need, S) == INV
-    assert f(A, 0, 4, 64, 64, A, NULL, 0, S) == WSERR
-    assert f(A, 0, 4, 64, 64, A, WS, 16, S) == WSERR
-    assert f(A, 0, 4, 64, 64, A, MIS8, need, S) == ALIGN
-    assert f(MIS1, 0, 4, 64, 64, A, WS, need, S) == ALIGN
+    assert f(A, 0, 4, 64, 64, NULL, S) == INV
+    assert f(A, 7, 4, 64, 64, A, S) == INV
+    assert f(A, 0, 4, 64, 60, A, S) == INV
+    assert f(NULL, 0, 4, 64, 64, A, S) == INV
+    assert f(MIS1, 0, 4, 64, 64, A, S) == ALIGN
+    assert f(A, 0, 4, 64, 64, MIS1, S) == ALIGN
 
 
 def test_product_refusals(no_gpu):
