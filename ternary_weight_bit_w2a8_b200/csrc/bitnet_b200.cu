@@ -1058,22 +1058,22 @@ int launch_fp4_small(DeviceInfo *dev, const uint8_t *codes, int xtype, const uin
 }
 
 // Weight rows per tile of the pair kernel: the width whose rounds over the
-// B200's 74 pairs take the fewest cycles.  Measured: a 256-k stage takes 352,
-// 425, 483 and 600 cycles for 64, 128, 192 and 256 rows (what an SM loads for
-// it, at 60 to 65 bytes a cycle; the MMAs take twice the rows), with NV scales
-// 192 and 256 rows 520 and 625; a tile costs some 500 more, one of 256 rows,
-// whose single accumulator has to be emptied first, 1500.  2048 x 2560 x 6912
-// NV takes 21.6 us with 192 rows, 23.4 with 256; 2048 x 9472 x 10240 takes
-// 81.0 and 69.6.
+// B200's 74 pairs take the least time.  Measured on 2048 x 9472 x K: a 256-k
+// stage of a tile takes kStage ns and the tile kEnd more (its accumulators are
+// emptied while the next tile's first MMAs wait, or run beside).  NV stages
+// bring more scales.  2048 x 13824 x 2560 MX takes 62, 38, 33, 30.0 and 29.7 us
+// with 64, 128, 192, 256 and 384 rows, 512 x 6912 x 2560 11.4, 9.9, 7.7, 8.8
+// and 10.8.
 int fp4_pair_width(int64_t M, int64_t N, int64_t K, int format) {
-    constexpr int kWidths[4] = {256, 192, 128, 64};
-    constexpr int kStage[2][4] = {{600, 483, 425, 352}, {625, 520, 425, 352}};
+    constexpr int kWidths[5] = {384, 256, 192, 128, 64};
+    constexpr int kStage[2][5] = {{490, 358, 288, 240, 207}, {520, 385, 345, 241, 207}};
+    constexpr int kEnd[5] = {1400, 760, 590, 410, 370};
     const int64_t nk = ceil_div(k_pad(K), kFp4StageK), tm = ceil_div(M, 256);
     int best = 256;
     int64_t cost = INT64_MAX;
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 5; ++i) {
         const int64_t rounds = ceil_div(tm * ceil_div(N, kWidths[i]), 74);
-        const int64_t c = rounds * (nk * kStage[format == BITNET_FP4_MX ? 0 : 1][i] + (i == 0 ? 1500 : 500));
+        const int64_t c = rounds * (nk * kStage[format == BITNET_FP4_MX ? 0 : 1][i] + kEnd[i]);
         if (c < cost) cost = c, best = kWidths[i];
     }
     return best;
@@ -1105,7 +1105,7 @@ int launch_fp4_pair(DeviceInfo *dev, const uint8_t *codes, const uint8_t *sa, co
                          kFp4TileBytes, kFp4TileBytes / 4, format == BITNET_FP4_MX ? 2 : 4, CU_TENSOR_MAP_SWIZZLE_NONE,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
     };
-    if (!fp4_code_map(&amap, codes, M, K, 128) || !fp4_code_map(&wmap, w, N, K, BT / 2) || !scale_map(&samap, sa, M) ||
+    if (!fp4_code_map(&amap, codes, M, K, 128) || !fp4_code_map(&wmap, w, N, K, BT > 192 ? BT / 4 : BT / 2) || !scale_map(&samap, sa, M) ||
         !scale_map(&swmap, sw, N))
         return BITNET_ERR_CUDA;
     Fp4PairArgs a{};
@@ -1122,6 +1122,7 @@ int launch_fp4_pair(DeviceInfo *dev, const uint8_t *codes, const uint8_t *sa, co
             case 64: return launch_fp4_pair_variant<F, 64>(dev, amap, wmap, samap, swmap, a, st);
             case 128: return launch_fp4_pair_variant<F, 128>(dev, amap, wmap, samap, swmap, a, st);
             case 192: return launch_fp4_pair_variant<F, 192>(dev, amap, wmap, samap, swmap, a, st);
+            case 384: return launch_fp4_pair_variant<F, 384>(dev, amap, wmap, samap, swmap, a, st);
             default: return launch_fp4_pair_variant<F, 256>(dev, amap, wmap, samap, swmap, a, st);
         }
     });

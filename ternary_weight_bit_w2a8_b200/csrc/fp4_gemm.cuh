@@ -147,6 +147,12 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same where no memory is handed over: nobody leaves, or goes on, early.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
 __device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
@@ -433,7 +439,7 @@ __global__ void __launch_bounds__(kFp4Threads, Fp4Small<FMT, BT>::kCtas)
             for (int i = 0; i < 4; ++i)
                 if (n + i < a.N) fp4_store(a.y, c * a.ldy + n + i, __fmul_rn(o[i], g), a.ytype);
         }
-        cluster_sync();  // nobody reads this CTA's shared memory any more
+        cluster_sync_relaxed();  // nobody reads this CTA's shared memory any more
     } else {
         __syncthreads();
     }

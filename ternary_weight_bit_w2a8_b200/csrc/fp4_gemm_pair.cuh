@@ -4,16 +4,19 @@
 // A pair of CTAs holds a tile of 256 tokens x BT weight rows: each CTA the
 // accumulators of its 128 tokens, in its shared memory the codes of those
 // tokens and of half the weight rows (the tensor cores read the other half
-// from the peer), and the scales of its tokens and of all BT weight rows.  So
-// a 256-k stage of a 256 x 256 tile brings 38 KB to an SM for 512 cycles of
-// MMAs; a tile of one SM would bring as much for half the work, more than an
-// SM can load from L2.
+// from the peer), and the scales of its tokens and of all BT weight rows.
+//   What bounds it: an SM takes in some 64 bytes a cycle from L2, and a 256-k
+// stage (16 KB of token codes, 64 BT bytes of weight codes, the scales) feeds
+// 2 BT cycles of MMAs.  64 to 192 rows are bound by the loads (352 to 483
+// cycles a stage), 384 rows by the MMAs (768).  Tiles of more than 192 rows are
+// multiplied in two halves with an accumulator each from the same token codes.
 //   Persistent: pairs take tiles in turn, tokens fastest, so that the pairs at
 // work share weight rows in L2.  Warp 0 of each CTA loads its part of a stage
 // and completes on the first CTA's barrier; warp 1 of the first CTA issues the
 // scale copies and MMAs of both; eight epilogue warps per CTA empty the
-// accumulators into registers as 16-bit values, release them and store rows
-// while the next tile runs (two accumulators where they fit: BT <= 192).
+// accumulators into registers, release them one by one and store rows while
+// the next tile runs (up to 192 rows it runs in the other accumulator, above
+// that the first half's MMAs run while the second half is emptied).
 #pragma once
 
 #include "fp4_gemm.cuh"
@@ -35,27 +38,33 @@ struct Fp4PairArgs {
 template <int FMT, int BT>
 struct Fp4Pair {
     static constexpr int kTiles = FMT == BITNET_FP4_MX ? 2 : 4;  // scale tiles per stage and 128 rows
-    // A tile starts on a multiple of 64 rows, so its weight scales may start in the middle of a 128-row band: two
-    // tensor-memory columns in.  (An odd column, as tiles of 96 or 160 rows would need, is refused by the MMA.)
+    // A tile starts on a multiple of 64 rows, and so does its second half, so their weight scales may start in the
+    // middle of a 128-row band: two tensor-memory columns in.  (An odd column, as tiles of 96 or 160 rows would need,
+    // is refused by the MMA.)
     static constexpr int kBands = (BT + 127) / 128;
-    static constexpr int kAcc = BT <= 192 ? 2 : 1;               // accumulators
+    static constexpr int kHalves = BT > 192 ? 2 : 1;
+    static constexpr int kCols = BT / kHalves;                   // columns of an accumulator; there are two
     static constexpr int kABytes = 128 * 128, kWBytes = BT / 2 * 128, kS = kTiles * kFp4TileBytes;
     static constexpr int kStage = kABytes + kWBytes + (1 + kBands) * kS;
     static constexpr int kOut = kFp4PairEpiWarps * 4096;         // a box of 32 rows x 128 bytes of y per warp
-    static constexpr int kStages = (224 * 1024 - kOut) / kStage < 8 ? (224 * 1024 - kOut) / kStage : 8;
+    // Tensor-memory columns of a stage's scales, and how many stages' fit beside the accumulators.  With as many as
+    // shared-memory stages, a stage's columns are free when its codes are; with fewer (two, for 192 and 384 rows of NV)
+    // the issuer also waits for older MMAs, some 90 cycles a stage (which 384 rows' 768 cycles hide).  So no more
+    // shared-memory stages than that, unless it leaves fewer than four.
+    static constexpr int kSlotCols = 4 * kTiles * (1 + kBands);
+    static constexpr int kFit = (512 - 2 * kCols) / kSlotCols;
+    static constexpr int kMost = kFit >= 4 && kFit < 8 ? kFit : 8;
+    static constexpr int kStages = (225 * 1024 - kOut) / kStage < kMost ? (225 * 1024 - kOut) / kStage : kMost;
     static constexpr int kOutAt = kStages * kStage;
     static constexpr int kBars = kOutAt + kOut;
     static constexpr int kBytes = kBars + (2 * kStages + 5) * 8 + 16;
-    // Tensor-memory columns of a stage's scales, and how many stages' fit beside the accumulators.  With as many as
-    // shared-memory stages, a stage's columns are free when its codes are; with fewer (192 columns of NV: 2) the issuer
-    // waits for older MMAs, which cost it 190 cycles a stage.
-    static constexpr int kSlotCols = 4 * kTiles * (1 + kBands);
-    static constexpr int kFit = (512 - kAcc * BT) / kSlotCols;
     static constexpr int kSlots = kFit < kStages ? kFit : kStages;
-    static constexpr int kNeed = kAcc * BT + kSlots * kSlotCols;
-    static constexpr int kCols = kNeed <= 256 ? 256 : 512;
-    static_assert(kNeed <= 512 && kStages >= 3 && kSlots >= 2 && BT % 64 == 0 && BT <= 256, "tile");
-    static_assert(kStage % 1024 == 0 && kWBytes % 1024 == 0, "swizzled rows");
+    static constexpr int kNeed = 2 * kCols + kSlots * kSlotCols;
+    static constexpr int kTmem = kNeed <= 256 ? 256 : 512;
+    static_assert(kNeed <= 512 && kStages >= 3 && kSlots >= 2 && kCols % 64 == 0 && kCols <= 192, "tile");
+    static_assert(kHalves == 1 || BT % 128 == 0, "whole bands");
+    static_assert(kStage % 1024 == 0 && kCols / 2 * 128 % 1024 == 0, "swizzled rows");
+    static_assert(kBytes + 1024 <= 232448, "shared memory");
 };
 
 // A TMA load of one CTA of a pair that completes on a barrier of either (an
@@ -103,8 +112,12 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t *bar) {
         : "memory");
 }
 
+// Arrives on a barrier of either CTA.  Release order at CTA scope is enough: what
+// it tells the other CTA is that tensor memory has been read (tcgen05.wait::ld
+// and the fence before), no memory; at cluster scope the arrival took 1000 to
+// 1700 cycles.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *v) {
@@ -130,19 +143,84 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return r;
 }
 
-// 32 * groups (1 or 2) accumulators of a lane times gs as a row of its warp's box: 128-byte
-// rows, 16-byte piece w of row r at piece w ^ (r % 8).
-template <int DT>
-__device__ __forceinline__ void box_rows(uint8_t *box, const uint32_t *f, int groups, float gs, int lane) {
+template <int DT, int N>
+__device__ __forceinline__ void pack_all(uint32_t (&v)[N], const uint32_t *f, float gs) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = pack2<DT>(__fmul_rn(__uint_as_float(f[2 * i]), gs), __fmul_rn(__uint_as_float(f[2 * i + 1]), gs));
+}
+
+// Stores 8 * pieces columns (64 or 32) of a warp's 32 rows, a lane's row as the
+// 16-bit pairs v[at], v[at + 1], ...: put down as 128-byte rows of shared memory
+// (16-byte piece w of row r at piece w ^ (r % 8), so that neither the lanes'
+// rows nor a row's pieces share banks) and stored from there, whole rows of
+// lines at a time.
+template <int N>
+__device__ __forceinline__ void store_box(const Fp4PairArgs &a, uint8_t *box, const uint32_t (&v)[N], int at, int pieces,
+                                          uint16_t *y, int rows, int64_t nb, int lane) {
+    __syncwarp();  // the rows of the last box have been read
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
-        if (w >= 4 * groups) break;
-        uint32_t t[4];
+        if (at + 4 * w >= N) break;
+        *reinterpret_cast<uint4 *>(box + lane * 128 + ((w ^ (lane & 7)) << 4)) =
+            make_uint4(v[at + 4 * w], v[at + 4 * w + 1], v[at + 4 * w + 2], v[at + 4 * w + 3]);
+    }
+    __syncwarp();
+    if (a.vec) {
+        const int w = lane & (pieces - 1), step = 32 / pieces;
+        const int64_t n = nb + 8 * w;
+        if (pieces == 8 && rows == 32 && nb + 64 <= a.N) {  // a whole box: every row is read before the first is stored
+            uint4 t[8];
+            const int r0 = lane >> 3;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            t[i] = pack2<DT>(__fmul_rn(__uint_as_float(f[8 * w + 2 * i]), gs),
-                             __fmul_rn(__uint_as_float(f[8 * w + 2 * i + 1]), gs));
-        *reinterpret_cast<uint4 *>(box + lane * 128 + ((w ^ (lane & 7)) << 4)) = make_uint4(t[0], t[1], t[2], t[3]);
+            for (int i = 0; i < 8; ++i)
+                t[i] = *reinterpret_cast<const uint4 *>(box + (r0 + 4 * i) * 128 + ((w ^ ((r0 + 4 * i) & 7)) << 4));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(y + (r0 + 4 * i) * a.ldy + n) = t[i];
+            return;
+        }
+        for (int r = lane / pieces; r < rows; r += step) {
+            const uint4 t = *reinterpret_cast<const uint4 *>(box + r * 128 + ((w ^ (r & 7)) << 4));
+            uint16_t *yp = y + r * a.ldy + n;
+            if (n + 8 <= a.N) {
+                *reinterpret_cast<uint4 *>(yp) = t;
+            } else {
+                const uint32_t q[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (n + e < a.N) yp[e] = (uint16_t)(q[e >> 1] >> (16 * (e & 1)));
+            }
+        }
+        return;
+    }
+    // A lane stores the pair of a row's values that lies on a 4-byte boundary
+    // of y; where the row starts between two, the last lane has the box's last
+    // value and its first.  Eight rows are read before the first is stored (one
+    // by one, a store holds up the next row's reads).
+    const int width = 8 * pieces, last = width / 2 - 1;
+    const int cols = (int)(a.N - nb < width ? a.N - nb : width);
+    auto value = [&](int r, int e) -> uint32_t {
+        return *reinterpret_cast<const uint16_t *>(box + r * 128 + (((e >> 3) ^ (r & 7)) << 4) + 2 * (e & 7));
+    };
+    const uintptr_t y0 = reinterpret_cast<uintptr_t>(y + nb) >> 1;
+    for (int r0 = 0; r0 < rows && lane <= last; r0 += 8) {
+        uint32_t pr[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = 2 * lane + (int)((y0 + (r0 + i) * a.ldy) & 1);
+            pr[i] = value(r0 + i, e) | value(r0 + i, (e + 1) & (width - 1)) << 16;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (r0 + i >= rows) break;
+            uint16_t *yr = y + (r0 + i) * a.ldy + nb;
+            const int odd = (int)((y0 + (r0 + i) * a.ldy) & 1), e = 2 * lane + odd;
+            if (e + 1 < cols)
+                *reinterpret_cast<uint32_t *>(yr + e) = pr[i];
+            else if (e < cols)
+                yr[e] = (uint16_t)pr[i];
+            if (odd && lane == last && cols > 0) yr[0] = (uint16_t)(pr[i] >> 16);
+        }
     }
 }
 
@@ -189,13 +267,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                     "r"(L::kCols)
+                     "r"(L::kTmem)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();  // both CTAs' barriers are set up
+    cluster_sync_relaxed();  // both CTAs' barriers are set up (and fenced)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
@@ -220,7 +298,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
                     const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * L::kStage);
                     tma_load_pair(st, &amap, i * 128, m0, bar);
-                    tma_load_pair(st + L::kABytes, &wmap, i * 128, (int)(n0 + rank * (BT / 2)), bar);
+#pragma unroll
+                    for (int h = 0; h < L::kHalves; ++h)
+                        tma_load_pair(st + L::kABytes + h * (L::kCols / 2 * 128), &wmap, i * 128,
+                                      (int)(n0 + h * L::kCols + rank * (L::kCols / 2)), bar);
                     uint8_t *ss = st + L::kABytes + L::kWBytes;
                     tma_load_pair(ss, &samap, 0, (m0 / 128) * tiles + i * L::kTiles, bar);
 #pragma unroll
@@ -238,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
         // ---------------------------------------------------------------- MMA issuer
         // One thread; what it does per stage has to stay below the MMAs' 2 BT cycles.
         if (rank == 0 && elect_one()) {
-            constexpr uint32_t idesc = fp4_idesc(FMT, 256, BT);
+            constexpr uint32_t idesc = fp4_idesc(FMT, 256, L::kCols);
             const uint32_t base = smem_u32(sm);
             const uint64_t a0 = umma_desc_sw128(base), w0 = umma_desc_sw128(base + L::kABytes);
             const uint64_t s0 = scale_desc(base + L::kABytes + L::kWBytes);
@@ -246,15 +327,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
             bool ok = true;
             int s = 0, slot = 0, g = 0, li = 0;
             uint32_t phase = 0;
-            for (int u = pair; ok && u < units; u += pairs, ++li) {
-                const int d = li % L::kAcc;
-                if (li >= L::kAcc && !tc_wait(&acc_empty[d], (uint32_t)(li / L::kAcc - 1) & 1u, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t dt = tmem + (uint32_t)(d * BT);
-                // rows into the first band of weight scales: 32 to a column
-                const uint32_t off = BT % 128 == 0 ? 0 : (uint32_t)((u / a.tiles_m) * BT % 128) / 32;
+            // use `use` of accumulator d waits until the use before has been read
+            auto acc_free = [&](int d, int use) {
+                if (use > 0 && !tc_wait(&acc_empty[d], (uint32_t)(use - 1) & 1u, abort_flag)) return false;
+                tc_fence_after();
+                return true;
+            };
+            for (int u = pair; u < units; u += pairs, ++li) {
+                // odd tiles of 64 or 192 rows start two columns into their first band of weight scales
+                const uint32_t off = BT % 128 == 0 ? 0 : 2 * ((uint32_t)(u / a.tiles_m) & 1);
+                const int d = L::kHalves == 2 ? 0 : li & 1;
+                if (L::kHalves == 1 && !(ok = acc_free(d, li >> 1))) break;
                 for (int i = 0; i < nk; ++i, ++g) {
                     if (!tc_wait(&full[s], phase, abort_flag) ||
                         (L::kSlots < S && g >= L::kSlots &&
@@ -264,8 +347,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
                     }
                     tc_fence_after();
                     const uint64_t at = (uint64_t)(s * (L::kStage >> 4));
-                    const uint32_t ca = tmem + (uint32_t)(L::kAcc * BT + slot * L::kSlotCols), cw = ca + 4 * L::kTiles;
+                    const uint32_t ca = tmem + (uint32_t)(2 * L::kCols + slot * L::kSlotCols), cw = ca + 4 * L::kTiles;
                     const bool whole = i < full_stages;
+                    const uint32_t more = i > 0 ? 1u : 0u;
 #pragma unroll
                     for (int t = 0; t < L::kTiles; ++t) {
                         if (t < L::kTiles / 2 || whole) {
@@ -276,19 +360,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
                                                     s0 + at + (uint64_t)(((1 + b) * L::kS + t * kFp4TileBytes) >> 4));
                         }
                     }
+                    auto multiply = [&](int h) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int t = FMT == BITNET_FP4_MX ? j >> 1 : j;
-                        const int id = FMT == BITNET_FP4_MX ? (j & 1) * 2 : 0;
-                        if (j < 2 || whole)
-                            umma_fp4_pair<FMT>(dt, a0 + at + 2 * j, w0 + at + 2 * j, idesc | fp4_scale_id(id), ca + 4 * t,
-                                               cw + 4 * t * L::kBands + off, j > 0 ? 1u : (uint32_t)(i > 0));
+                        for (int j = 0; j < 4; ++j) {
+                            const int t = FMT == BITNET_FP4_MX ? j >> 1 : j;
+                            const int id = FMT == BITNET_FP4_MX ? (j & 1) * 2 : 0;
+                            if (j < 2 || whole)
+                                umma_fp4_pair<FMT>(tmem + (uint32_t)((d + h) * L::kCols), a0 + at + 2 * j,
+                                                   w0 + at + (uint64_t)(h * (L::kCols / 2 * 128) >> 4) + 2 * j,
+                                                   idesc | fp4_scale_id(id), ca + 4 * t,
+                                                   cw + 4 * t * L::kBands + off + h * (L::kCols / 32), j > 0 ? 1u : more);
+                        }
+                    };
+                    if (L::kHalves == 2 && i == 0 && !(ok = acc_free(0, li))) break;
+                    multiply(0);
+                    if constexpr (L::kHalves == 2) {
+                        if (i + 1 == nk) umma_commit_pair(&acc_full[0]);
+                        if (i == 0 && !(ok = acc_free(1, li))) break;
+                        multiply(1);
                     }
                     umma_commit_pair(&empty[s]);
                     if (++s == S) s = 0, phase ^= 1;
                     if (++slot == L::kSlots) slot = 0;
                 }
-                if (ok) umma_commit_pair(&acc_full[d]);
+                if (!ok) break;
+                umma_commit_pair(&acc_full[L::kHalves == 2 ? 1 : d]);
             }
             if (!ok) {
                 // the MMAs issued so far end before tensor memory is freed
@@ -299,100 +395,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- epilogue
-        // Two warps share a lane quarter: the first takes the first half of the tile's 32-column groups (rounded up),
-        // the second the rest.  The accumulator is released as soon as its values are in registers; they are put
-        // down as 16-bit values 64 columns at a time as 128-byte rows of shared memory (16-byte pieces swizzled, so that neither the
-        // lanes' rows nor a row's pieces share banks) and stored from there, whole rows of lines at a time.
-        constexpr int kGroups = BT / 32, kMost = (kGroups + 1) / 2;
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
-        const int groups = half == 0 ? kMost : kGroups - kMost;
-        const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * kMost * 32);
+        // Two warps share a lane quarter: the first takes the first half of an accumulator's 32-column groups (rounded
+        // up), the second the rest.
+        constexpr int kGroups = L::kCols / 32, kMost = (kGroups + 1) / 2;
+        const int quarter = warp & 3, part = (warp - 2) >> 2;
+        const int groups = part == 0 ? kMost : kGroups - kMost;
+        const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(part * kMost * 32);
         uint8_t *box = sm + L::kOutAt + (warp - 2) * 4096;
         const float gs = (a.ga != nullptr ? *a.ga : 1.0f) * (a.gw != nullptr ? *a.gw : 1.0f);
-        int li = 0;
-        for (int u = pair; u < units; u += pairs, ++li) {
-            const int d = li % L::kAcc;
-            if (!warp_wait(&acc_full[d], (uint32_t)(li / L::kAcc) & 1u, abort_flag)) break;
+        // waits for use `use` of accumulator d, reads this warp's part of it as 16-bit pairs and releases it
+        auto empty_acc = [&](int d, int use, uint32_t (&v)[16 * kMost]) -> bool {
+            if (!warp_wait(&acc_full[d], (uint32_t)use & 1u, abort_flag)) return false;
             tc_fence_after();
             uint32_t f[32 * kMost];
 #pragma unroll
             for (int c = 0; c < kMost; ++c)
-                if (c < groups) tmem_ld32(t0 + (uint32_t)(d * BT + 32 * c), f + 32 * c);
+                if (c < groups) tmem_ld32(t0 + (uint32_t)(d * L::kCols + 32 * c), f + 32 * c);
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&acc_empty[d]), 0));
-            const int tm = u % a.tiles_m;
-            const int64_t m0 = (int64_t)tm * 256 + rank * 128 + quarter * 32;
-            const int64_t n0 = (int64_t)(u / a.tiles_m) * BT + half * kMost * 32;
+            if (a.ytype == BITNET_FP16)
+                pack_all<BITNET_FP16, 16 * kMost>(v, f, gs);
+            else
+                pack_all<BITNET_BF16, 16 * kMost>(v, f, gs);
+            return true;
+        };
+        // stores this warp's part: rows of tokens from m0, columns of y from n0
+        auto store = [&](int64_t m0, int64_t n0, const uint32_t (&v)[16 * kMost]) {
             const int rows = (int)(a.M - m0 < 32 ? a.M - m0 : 32);
             uint16_t *y = static_cast<uint16_t *>(a.y) + m0 * a.ldy;
 #pragma unroll
             for (int c = 0; c < kMost; c += 2) {
                 if (c >= groups) break;
-                const int pieces = c + 1 < groups ? 8 : 4;  // of 8 columns to a row
-                __syncwarp();                               // the rows of the last round have been read
-                if (a.ytype == BITNET_FP16)
-                    box_rows<BITNET_FP16>(box, f + 32 * c, kMost - c < 2 ? 1 : 2, gs, lane);
-                else
-                    box_rows<BITNET_BF16>(box, f + 32 * c, kMost - c < 2 ? 1 : 2, gs, lane);
-                __syncwarp();
-                const int64_t nb = n0 + 32 * c;
-                if (a.vec) {
-                    const int w = lane & (pieces - 1), step = 32 / pieces;
-                    const int64_t n = nb + 8 * w;
-                    for (int r = lane / pieces; r < rows; r += step) {
-                        const uint4 t = *reinterpret_cast<const uint4 *>(box + r * 128 + ((w ^ (r & 7)) << 4));
-                        uint16_t *yp = y + r * a.ldy + n;
-                        if (n + 8 <= a.N) {
-                            *reinterpret_cast<uint4 *>(yp) = t;
-                        } else {
-                            const uint32_t q[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (n + e < a.N) yp[e] = (uint16_t)(q[e >> 1] >> (16 * (e & 1)));
-                        }
-                    }
-                } else {
-                    // A lane stores the pair of a row's values that lies on a 4-byte boundary of y; where the row starts
-                    // between two, the last lane has the box's last value and its first.  Eight rows are read before
-                    // the first is stored (one by one, a store holds up the next row's reads).
-                    const int width = 8 * pieces, last = width / 2 - 1;
-                    const int cols = (int)(a.N - nb < width ? a.N - nb : width);
-                    auto value = [&](int r, int e) -> uint32_t {
-                        return *reinterpret_cast<const uint16_t *>(box + r * 128 + (((e >> 3) ^ (r & 7)) << 4) + 2 * (e & 7));
-                    };
-                    const uintptr_t y0 = reinterpret_cast<uintptr_t>(y + nb);
-                    for (int r0 = 0; r0 < rows && lane <= last; r0 += 8) {
-                        uint32_t pr[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int e = 2 * lane + (int)((y0 >> 1) + (r0 + i) * a.ldy & 1);
-                            pr[i] = value(r0 + i, e) | value(r0 + i, (e + 1) & (width - 1)) << 16;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            if (r0 + i >= rows) break;
-                            uint16_t *yr = y + (r0 + i) * a.ldy + nb;
-                            const int odd = (int)((y0 >> 1) + (r0 + i) * a.ldy & 1), e = 2 * lane + odd;
-                            if (e + 1 < cols)
-                                *reinterpret_cast<uint32_t *>(yr + e) = pr[i];
-                            else if (e < cols)
-                                yr[e] = (uint16_t)pr[i];
-                            if (odd && lane == last && cols > 0) yr[0] = (uint16_t)(pr[i] >> 16);
-                        }
-                    }
-                }
+                store_box(a, box, v, 16 * c, c + 1 < groups ? 8 : 4, y, rows, n0 + 32 * c, lane);
+            }
+        };
+        int li = 0;
+        for (int u = pair; u < units; u += pairs, ++li) {
+            const int64_t m0 = (int64_t)(u % a.tiles_m) * 256 + rank * 128 + quarter * 32;
+            const int64_t n0 = (int64_t)(u / a.tiles_m) * BT + part * kMost * 32;
+            uint32_t v[16 * kMost];
+            if constexpr (L::kHalves == 1) {
+                if (!empty_acc(li & 1, li >> 1, v)) break;
+                store(m0, n0, v);
+            } else {
+                // both halves are emptied before the first is stored: the next tile waits for them
+                uint32_t v1[16 * kMost];
+                if (!empty_acc(0, li, v) || !empty_acc(1, li, v1)) break;
+                store(m0, n0, v);
+                store(m0, n0 + L::kCols, v1);
             }
         }
         __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();  // neither CTA signals the other or reads its shared memory any more
+    cluster_sync_relaxed();  // neither CTA signals the other or reads its shared memory any more
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::kCols) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::kTmem) : "memory");
     }
 }
 
