@@ -1390,7 +1390,7 @@ BITNET_API int bitnet_fp4_tensor_scale(const void *x, int dtype, int64_t rows, i
         constexpr int D = decltype(dt)::value;
         using T = typename Fp4Type<D>::T;
         int64_t blocks = ceil_div(rows * ceil_div(K, kFp4ScalePiece<D>), kThreads / 32);
-        if (blocks > 4 * dev->sm_count) blocks = 4 * dev->sm_count;
+        if (blocks > 8 * dev->sm_count) blocks = 8 * dev->sm_count;
         if (blocks < 1) blocks = 1;
         if (blocks > 1) {
             const int rc1 = launched(launch_pdl(fp4_clear_kernel, dim3(1), dim3(1), (size_t)0, st, g));

@@ -51,6 +51,29 @@ struct Fp4Type<BITNET_FP32> {
     static __device__ __forceinline__ T from_f(float v) { return v; }
 };
 
+// Pairs of fp32 numbers in one 64-bit register: an instruction works on both,
+// rounding each as its single form does.
+__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 f2_unpack(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 // 32 bytes of a row as they are stored: 16 values, or 8 of fp32.
 template <int DT>
 struct Fp4Raw {
@@ -122,6 +145,14 @@ template <int DT>
 __device__ __forceinline__ float fp4_value(const Fp4Raw<DT> &v, int i) {
     return Fp4Type<DT>::to_f(reinterpret_cast<const typename Fp4Type<DT>::T *>(v.w)[i]);
 }
+// Values 2i and 2i + 1 as a pair of fp32.
+template <int DT>
+__device__ __forceinline__ uint64_t fp4_pair(const Fp4Raw<DT> &v, int i) {
+    if constexpr (DT == BITNET_BF16)
+        return (uint64_t)(v.w[i] & 0xffff0000u) << 32 | (v.w[i] << 16);
+    else
+        return f2_pack(fp4_value<DT>(v, 2 * i), fp4_value<DT>(v, 2 * i + 1));
+}
 
 // ------------------------------------------------------------------ rounding
 // e4m3 of a >= 0 (finite), to nearest even, saturating at 448.
@@ -143,8 +174,9 @@ __device__ __forceinline__ float e8m0_value(uint32_t b) {
     return __uint_as_float(b == 255u ? 0x7fc00000u : (b == 0u ? 0x00400000u : b << 23));
 }
 
-// Eight e2m1 codes (to nearest even, saturating at 6), v[0] in the low bits.
-__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+// Eight e2m1 codes (to nearest even, saturating at 6), the first in the low
+// bits.
+__device__ __forceinline__ uint32_t e2m1x8(const float2 (&v)[4]) {
     uint32_t r;
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
@@ -153,7 +185,7 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
         "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
         "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
         : "=r"(r)
-        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+        : "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y));
     return r;
 }
 
@@ -205,11 +237,17 @@ __device__ __forceinline__ Fp4Scale fp4_scale(uint32_t top) {
     return q;
 }
 
+// The codes of eight values x (in pairs) of a block: z = x * inv, then z / s.
 template <int FMT>
-__device__ __forceinline__ uint32_t fp4_codes8(const float (&z)[8], const Fp4Scale &q, bool finite) {
-    float v[8];
+__device__ __forceinline__ uint32_t fp4_codes8(const uint64_t (&x)[4], float inv, const Fp4Scale &q, bool finite) {
+    const uint64_t inv2 = f2_pack(inv, inv), r2 = f2_pack(q.r, q.r), ns2 = f2_pack(-q.s, -q.s);
+    float2 v[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = FMT == BITNET_FP4_MX ? __fmul_rn(z[i], q.r) : div_exact(z[i], q.s, q.r);
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t z = f2_mul(x[i], inv2), t = f2_mul(z, r2);
+        // MX: exact; NV: div_exact
+        v[i] = f2_unpack(FMT == BITNET_FP4_MX ? t : f2_fma(f2_fma(t, ns2, z), r2, t));
+    }
     const uint32_t c = e2m1x8(v);
     return finite ? c : 0u;
 }
@@ -301,10 +339,10 @@ __global__ void __launch_bounds__(kThreads) fp4_quant_kernel(const typename Fp4T
             uint32_t c[V / 8];
 #pragma unroll
             for (int h = 0; h < V / 8; ++h) {
-                float z[8];
+                uint64_t p[4];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) z[j] = __fmul_rn(fp4_value<DT>(v[i], 8 * h + j), inv);
-                c[h] = fp4_codes8<FMT>(z, q, top < 0x7f800000u);
+                for (int j = 0; j < 4; ++j) p[j] = fp4_pair<DT>(v[i], 4 * h + j);
+                c[h] = fp4_codes8<FMT>(p, inv, q, top < 0x7f800000u);
             }
             if (stored) {
                 if constexpr (V == 16)
@@ -327,11 +365,33 @@ __global__ void __launch_bounds__(kThreads) fp4_quant_kernel(const typename Fp4T
 // ------------------------------------------------------------------ reading back
 // y[r, k] = round(fl32(element * scale) * g); element * scale is exact.
 
-// The value of a code: its three magnitude bits as exponent and mantissa of an
-// fp32 number stand for the e2m1 value times 2^-126 (subnormals included).
-__device__ __forceinline__ float e2m1_value(uint32_t code) {
-    const float e = __uint_as_float((code & 7u) << 22) * 8.507059173023462e37f;  // 2^126
-    return __uint_as_float(__float_as_uint(e) | ((code & 8u) << 28));
+// The eight values of a word of codes as pairs of fp32.
+__device__ __forceinline__ void e2m1_values8(uint32_t c, uint64_t (&v)[4]) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(c));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+        v[i] = f2_pack(f.x, f.y);
+    }
+}
+
+// Two fp32 values as two of the type, packed (one of fp32 at a time).
+template <int DT>
+__device__ __forceinline__ uint32_t fp4_round2(float2 v) {
+    uint32_t r;
+    if (DT == BITNET_FP16)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
+    else
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(v.y), "f"(v.x));
+    return r;
 }
 
 // A CTA reads a patch of 128 rows x 256 k; a lane takes 32 bytes of a row of y
@@ -383,11 +443,21 @@ __global__ void __launch_bounds__(kThreads) fp4_dequant_kernel(const uint8_t *__
             const int r = r0 + i * kStep;
             if (ALIGNED && (r >= nrows || k >= cols)) continue;
             const float s = FMT == BITNET_FP4_MX ? e8m0_value(sb[i]) : e4m3_value(sb[i]);
-            alignas(16) T t[V];
+            uint32_t w[8];
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                t[j] = Fp4Type<DT>::from_f(__fmul_rn(__fmul_rn(e2m1_value(c[i][j / 8] >> (4 * (j & 7))), s), gs));
-            const uint32_t *w = reinterpret_cast<const uint32_t *>(t);
+            for (int h = 0; h < V / 8; ++h) {
+                uint64_t e[4];
+                e2m1_values8(c[i][h], e);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = f2_unpack(f2_mul(f2_mul(e[j], f2_pack(s, s)), f2_pack(gs, gs)));
+                    if constexpr (sizeof(T) == 4)
+                        w[2 * j] = __float_as_uint(f.x), w[2 * j + 1] = __float_as_uint(f.y);
+                    else
+                        w[4 * h + j] = fp4_round2<DT>(f);
+                }
+            }
+            const T *t = reinterpret_cast<const T *>(w);
             T *yr = y + r * ldy;
             if constexpr (ALIGNED) {
                 if (wide && k + V <= cols) {
@@ -399,7 +469,7 @@ __global__ void __launch_bounds__(kThreads) fp4_dequant_kernel(const uint8_t *__
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if (k + (h + 1) * (V / 2) <= cols) {
-                        reinterpret_cast<uint4 *>(yr + k)[h] = reinterpret_cast<const uint4 *>(t)[h];
+                        reinterpret_cast<uint4 *>(yr + k)[h] = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
                     } else {
 #pragma unroll
                         for (int j = h * (V / 2); j < (h + 1) * (V / 2); ++j)
@@ -444,7 +514,7 @@ __global__ void __launch_bounds__(kThreads) fp4_dequant_kernel(const uint8_t *__
 // own values: they meet in an atomic maximum of the bits (positive floats order
 // as their bits do; a maximum does not depend on the order), g having been set
 // to 0 by a launch before; one CTA alone stores it.  A warp takes a piece of a
-// row at a time, eight 32-byte loads to a lane; the values before the row's
+// row at a time, four 32-byte loads to a lane; the values before the row's
 // first 32-byte boundary and behind its last are taken one by one.
 __global__ void fp4_clear_kernel(float *g) {
     pdl_wait();
@@ -452,7 +522,7 @@ __global__ void fp4_clear_kernel(float *g) {
     *g = 0.0f;
 }
 
-constexpr int kFp4ScaleLoads = 8;
+constexpr int kFp4ScaleLoads = 4;
 template <int DT>
 constexpr int kFp4ScalePiece = Fp4Raw<DT>::kValues * 32 * kFp4ScaleLoads;
 

@@ -237,10 +237,10 @@ __device__ __forceinline__ void fp4_quantise_stages(const Fp4SmallArgs &a, uint8
             uint32_t c[V / 8];
 #pragma unroll
             for (int h = 0; h < V / 8; ++h) {
-                float z[8];
+                uint64_t p[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) z[e] = __fmul_rn(fp4_value<XT>(v[t], 8 * h + e), inv);
-                c[h] = fp4_codes8<FMT>(z, sc, top < 0x7f800000u);
+                for (int e = 0; e < 4; ++e) p[e] = fp4_pair<XT>(v[t], 4 * h + e);
+                c[h] = fp4_codes8<FMT>(p, inv, sc, top < 0x7f800000u);
             }
             // 16-byte piece p of token m lies at piece p ^ (m % 8) of its row
             const int byte = V / 2 * lane;
