@@ -259,7 +259,9 @@ __device__ __forceinline__ uint32_t fp4_codes8(const uint64_t (&x)[4], float inv
 // maximum by shuffles.  A lane asks for four rows before it uses the first
 // (128 bytes in flight: 13824 x 5120 bf16 into NV takes 39 us, one row at a
 // time 53).  Scale bytes are put together in shared memory; the rows of the
-// last band past the matrix get scale 0.
+// last band past the matrix get scale 0.  The CTAs start at the matrix's end:
+// where the tensor scale has just read it, that is what L2 still holds (2 % for
+// 13824 x 5120).
 //   ALIGNED: rows of x start on 16-byte boundaries.  Otherwise a warp reads a
 // row's values in order, one to a lane, and shared memory turns them round.
 constexpr int kFp4PatchK = 256;
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(kThreads) fp4_quant_kernel(const typename Fp4T
     __shared__ alignas(16) T turn[ALIGNED ? 1 : kStep * kFp4PatchK];
     const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
     const int64_t patches_k = ceil_div(k_pad(K), kFp4PatchK);
-    const int64_t band = (int64_t)blockIdx.x / patches_k, pk = (int64_t)blockIdx.x % patches_k;
+    const int64_t block = gridDim.x - 1 - blockIdx.x, band = block / patches_k, pk = block % patches_k;
     const int64_t row_bytes = fp4_row_bytes(K), tiles = fp4_scale_tiles(K, FMT);
     const int64_t k = pk * kFp4PatchK + V * lane;
     const bool wide = ((reinterpret_cast<uintptr_t>(x) | (uintptr_t)(ldx * (int64_t)sizeof(T))) & 31) == 0;
