@@ -102,8 +102,8 @@ __device__ __forceinline__ void fp4_store(void *y, int64_t i, float v, int dtype
 // rank order, each for its share of the rows.  No workspace, no atomics, and
 // the same bits every time.  Three CTAs fit an SM (two from 17 tokens up), so
 // that one's start and end overlap the others' loads.
-//   Before the launch-chain wait the first boxes of the weights are only asked
-// into L2: what an earlier kernel still writes is read after the wait.
+//   Before the launch-chain wait weights are only asked into L2: what an earlier
+// kernel still writes is read after the wait.
 //   QX: up to 16 tokens of x are quantised by the epilogue warps stage by
 // stage, straight into the swizzled operand rows and scale tiles, with the
 // arithmetic of fp4_quant_kernel.
@@ -117,6 +117,7 @@ struct Fp4SmallArgs {
     const float *ga, *gw;
     void *y;
     int split;               // CTAs per cluster
+    int prefetch;            // stages of weights asked into L2 before the launch-chain wait
 };
 
 template <int FMT, int BT>
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(kFp4Threads, Fp4Small<FMT, BT>::kCtas)
     if (threadIdx.x == 0) {
         prefetch_tensormap(&wmap);
         if (!QX) prefetch_tensormap(&amap);
-        for (int i = 0; i < n_i && i < S; ++i) {
+        for (int i = 0; i < n_i && i < a.prefetch; ++i) {
             tma_prefetch_2d(&wmap, (i0 + i) * 128, tile * kFp4Rows);
             prefetch_l2_bulk(sw + (int64_t)(i0 + i) * L::kS, scale_bytes(i0 + i));
         }
