@@ -1038,13 +1038,6 @@ int launch_fp4_small_variant(DeviceInfo *dev, const CUtensorMap &wmap, const CUt
 int launch_fp4_small(DeviceInfo *dev, const uint8_t *codes, int xtype, const uint8_t *w, int format, Fp4SmallArgs a,
                      cudaStream_t st) {
     a.split = fp4_split(a.N, a.K);
-    // Stages asked into L2 while the kernel before ends: all of a short range,
-    // three where the CTAs fill the SMs, so that they start as the kernel
-    // before runs out; else none, since they would all be there early and take
-    // its bandwidth.  With none, 3 and 6: 1 x 2560 x 6912 MX 5.1, 5.0, 4.6 us;
-    // 1 x 27648 x 5120 13.6, 14.3, 15.0; 1 x 55296 x 5120 24.1, 23.2, 22.7.
-    const int64_t stages = ceil_div(ceil_div(k_pad(a.K), kFp4StageK), a.split);
-    a.prefetch = stages <= 4 ? 4 : (ceil_div(a.N, kFp4Rows) * a.split >= 296 ? 3 : 0);
     const int BT = a.M <= 16 ? 16 : (a.M <= 32 ? 32 : 64);
     CUtensorMap wmap, amap;
     memset(&amap, 0, sizeof(amap));

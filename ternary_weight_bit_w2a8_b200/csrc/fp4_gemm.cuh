@@ -21,6 +21,7 @@ constexpr int kFp4StageK = 256;   // k per stage: a 128-byte swizzled row of cod
 constexpr int kFp4Threads = 192;  // producer, MMA issuer, 4 epilogue (and quantiser) warps
 constexpr int kFp4MaxSplit = 8;   // largest portable cluster
 constexpr int kFp4FusedTokens = 16;
+constexpr int kFp4Prefetch = 4;  // stages of weights asked into L2 before the launch-chain wait
 
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
     asm volatile(
@@ -102,8 +103,12 @@ __device__ __forceinline__ void fp4_store(void *y, int64_t i, float v, int dtype
 // rank order, each for its share of the rows.  No workspace, no atomics, and
 // the same bits every time.  Three CTAs fit an SM (two from 17 tokens up), so
 // that one's start and end overlap the others' loads.
-//   Before the launch-chain wait weights are only asked into L2: what an earlier
-// kernel still writes is read after the wait.
+//   Launch chain: before the wait for the kernel before, the first weights are
+// only asked into L2 (what that kernel still writes is read after the wait).
+// The next kernel may start once this one has asked for its last weights: its
+// CTAs then find room and warm L2 while this one multiplies, exchanges and
+// stores (1 x 13824 x 5120 MX 8.9 -> 8.0 us); started with this one's first
+// loads they took its bandwidth instead (9.2 us).
 //   QX: up to 16 tokens of x are quantised by the epilogue warps stage by
 // stage, straight into the swizzled operand rows and scale tiles, with the
 // arithmetic of fp4_quant_kernel.
@@ -117,7 +122,6 @@ struct Fp4SmallArgs {
     const float *ga, *gw;
     void *y;
     int split;               // CTAs per cluster
-    int prefetch;            // stages of weights asked into L2 before the launch-chain wait
 };
 
 template <int FMT, int BT>
@@ -292,7 +296,7 @@ __global__ void __launch_bounds__(kFp4Threads, Fp4Small<FMT, BT>::kCtas)
     if (threadIdx.x == 0) {
         prefetch_tensormap(&wmap);
         if (!QX) prefetch_tensormap(&amap);
-        for (int i = 0; i < n_i && i < a.prefetch; ++i) {
+        for (int i = 0; i < n_i && i < kFp4Prefetch; ++i) {
             tma_prefetch_2d(&wmap, (i0 + i) * 128, tile * kFp4Rows);
             prefetch_l2_bulk(sw + (int64_t)(i0 + i) * L::kS, scale_bytes(i0 + i));
         }
@@ -325,9 +329,9 @@ __global__ void __launch_bounds__(kFp4Threads, Fp4Small<FMT, BT>::kCtas)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
-    pdl_launch_dependents();
 
     if (warp == 0) {
+        if (n_i <= S) pdl_launch_dependents();
         int i = 0;
         for (; i < n_i; ++i) {
             const int s = i % S, gi = i0 + i;
@@ -346,6 +350,7 @@ __global__ void __launch_bounds__(kFp4Threads, Fp4Small<FMT, BT>::kCtas)
             }
             __syncwarp();
         }
+        if (n_i > S) pdl_launch_dependents();
         // no copy may still be landing when the CTA leaves (QX: a stage's
         // barrier also waits for the quantisers, which stop on an abort; the
         // wait is bounded)
