@@ -200,19 +200,21 @@ BITNET_API int bitnet_w2a8_gemm_noalloc(const int8_t *q, const uint8_t *packed, 
 
 /*
  * ------------------------------------------------------------------ 4-bit floating point
- * Microscaled 4-bit floating point, for the layers that are not ternary (the
- * pages have no counterpart).  Elements are e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ * Microscaled 4-bit floating point, for the layers of a model that are not
+ * ternary, its head for one (the pages have no counterpart).  Elements are e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6
  * and their negatives (codes 0..7, bit 3 the sign).  Two formats:
  *   BITNET_FP4_MX  blocks of 32 along K share an e8m0 scale 2^(byte - 127)
- *   BITNET_FP4_NV  blocks of 16 along K share an e4m3 scale
+ *   BITNET_FP4_NV  blocks of 16 along K share an e4m3 scale (sign bit 0)
  * and, with either, an optional fp32 tensor scale g (NULL = 1).  A matrix
  * [rows, K] is stored as
  *   codes   rows of K_pad / 2 bytes, K_pad = 128 * ceil(K / 128); the even k of
- *           a byte in its low half; K <= k < K_pad holds code 0
+ *           a byte in its low half; K <= k < K_pad holds code 0 (and its blocks
+ *           no NaN scale)
  *   scales  tiles of 128 rows x 4 blocks, 512 bytes: row r and block c of a tile
  *           at byte 16 * (r mod 32) + 4 * (r / 32) + c; the tiles of a 128-row
  *           band follow one another (K_pad / 128 of them for MX, K_pad / 64 for
- *           NV), then the next band; rows past the matrix hold byte 0
+ *           NV), then the next band.  bitnet_fp4_quant sets rows past the matrix
+ *           to 0; nothing depends on them
  * and stands for element * scale * g.
  */
 enum { BITNET_FP4_MX = 0, BITNET_FP4_NV = 1 };
@@ -287,7 +289,8 @@ BITNET_API int bitnet_fp4_gemm(const uint8_t *a, const uint8_t *a_scales, const 
  * (it may be NULL); more are quantised into it first.
  *   x, ldx       as in bitnet_fp4_quant; the rest as in bitnet_fp4_gemm
  *   workspace    device, >= bitnet_fp4_workspace_bytes(M, N, K, format) bytes,
- *                256-byte aligned
+ *                256-byte aligned; calls that may overlap on the GPU need one
+ *                each
  */
 BITNET_API int bitnet_fp4_linear(const void *x, int xdtype, int64_t ldx, const float *ga, const uint8_t *w,
                                  const uint8_t *w_scales, const float *gw, int format, void *y, int ydtype, int64_t M,

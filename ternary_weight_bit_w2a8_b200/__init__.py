@@ -265,6 +265,8 @@ class _on:
     allocates belongs to the stream that it runs on."""
 
     def __init__(self, index, stream):
+        if stream is not None and stream.device_index != index:
+            raise ValueError("stream must be one of the device that the tensors are on")
         self.device = _torch.cuda.device(index)
         self.stream = None if stream is None else _torch.cuda.stream(stream)
 

@@ -162,7 +162,7 @@ SHAPES = [(1, 1, 1), (1, 128, 128), (1, 2560, 2560), (2, 129, 64), (3, 300, 1000
           (17, 640, 512), (31, 96, 4100), (64, 513, 2560), (65, 100, 130), (100, 777, 1024), (128, 1000, 260),
           (129, 333, 700), (200, 1000, 2560), (257, 129, 5120), (513, 1100, 384), (1000, 640, 65), (1, 5, 20000),
           (600, 600, 600), (300, 20000, 256), (2100, 5000, 512), (520, 9700, 1000), (1030, 11111, 192),
-          (510, 7001, 3000), (2048, 2560, 2000)]
+          (510, 7001, 3000), (2048, 2560, 2000), (700, 4700, 256)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -277,3 +277,101 @@ def test_layers_in_a_graph_on_another_stream():
     y = bn.bitnet_fp4_linear(x, ws[0][0], ws[0][1], fmt, gw=ws[0][2], stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(y, bn.bitnet_fp4_linear(x, ws[0][0], ws[0][1], fmt, gw=ws[0][2]))
+
+
+def quantised_weight(N, K, fmt, seed):
+    W = (torch.randn(N, K, generator=torch.Generator().manual_seed(seed)) * 0.02).cuda()
+    return bn.bitnet_fp4_quant(W, fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_calls_that_overlap(fmt):
+    """Products of both kernels and fused layers on two streams at once, and two graphs replayed at once: the bits of
+    the calls one by one, again and again."""
+    gen = torch.Generator().manual_seed(7)
+    shapes = [(1, 2560, 6912), (12, 1000, 2560), (150, 3000, 1280), (1, 300, 700)]
+    work = []
+    for i, (M, N, K) in enumerate(shapes):
+        x = torch.randn(M, K, generator=gen).to(torch.bfloat16).cuda()
+        w, s = quantised_weight(N, K, fmt, i)
+        work.append((x, w, s, bn.bitnet_fp4_linear(x, w, s, fmt)))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = []
+    for rep in range(20):
+        for j, st in enumerate(streams):
+            x, w, s, want = work[(rep + j) % len(work)]
+            with torch.cuda.stream(st):
+                outs.append((bn.bitnet_fp4_linear(x, w, s, fmt), want))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in outs)
+    graphs = []
+    for j in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ys = [bn.bitnet_fp4_linear(x, w, s, fmt) for x, w, s, _ in work[2 * j:2 * j + 2]]
+        graphs.append((g, ys))
+    for rep in range(5):
+        for (g, ys), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for j, (g, ys) in enumerate(graphs):
+        assert all(torch.equal(y, work[2 * j + i][3]) for i, y in enumerate(ys))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_weights_written_just_before(fmt, M):
+    """A layer right behind the kernels that write its weights and its tokens, again and again into the same buffers:
+    nothing of the values before is read."""
+    N, K = 1300, 2560
+    codes = torch.empty(N, K // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.empty(bn.bitnet_fp4_scale_bytes(N, K, fmt), dtype=torch.uint8, device="cuda")
+    Ws = [(torch.randn(N, K, generator=torch.Generator().manual_seed(i)) * 0.02).cuda() for i in range(3)]
+    xs = [torch.randn(M, K, generator=torch.Generator().manual_seed(9 + i)).to(torch.bfloat16).cuda() for i in range(3)]
+    want = []
+    for W, x in zip(Ws, xs):
+        w, s = bn.bitnet_fp4_quant(W, fmt)
+        torch.cuda.synchronize()
+        want.append(bn.bitnet_fp4_linear(x, w, s, fmt))
+        torch.cuda.synchronize()
+    x = torch.empty_like(xs[0])
+    got = []
+    for rep in range(30):
+        x.copy_(xs[rep % 3])
+        bn.bitnet_fp4_quant(Ws[rep % 3], fmt, codes=codes, scales=scales)
+        got.append(bn.bitnet_fp4_linear(x, codes, scales, fmt))
+    for rep, y in enumerate(got):
+        assert torch.equal(y, want[rep % 3]), rep
+
+
+def test_binding_refuses_what_does_not_fit():
+    w, s = quantised_weight(64, 256, ref.MX, 0)
+    x = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
+    ok = bn.bitnet_fp4_linear(x, w, s, ref.MX)
+    assert ok.shape == (4, 64)
+    bad = [lambda: bn.bitnet_fp4_linear(x[:, :200], w, s, ref.NV),            # NV needs twice the scales
+           lambda: bn.bitnet_fp4_linear(x.to(torch.int8), w, s, ref.MX),
+           lambda: bn.bitnet_fp4_linear(x.t(), w, s, ref.MX),
+           lambda: bn.bitnet_fp4_linear(x, w.cpu(), s, ref.MX),
+           lambda: bn.bitnet_fp4_linear(x, w[:, :64], s, ref.MX),
+           lambda: bn.bitnet_fp4_linear(x, w, s[:-1], ref.MX),
+           lambda: bn.bitnet_fp4_linear(x, w, s, 2),
+           lambda: bn.bitnet_fp4_linear(x, w, s, ref.MX, ga=torch.ones(1)),
+           lambda: bn.bitnet_fp4_linear(x, w, s, ref.MX, y=torch.empty(4, 63, device="cuda")),
+           lambda: bn.bitnet_fp4_quant(x, ref.MX, codes=w),
+           lambda: bn.bitnet_fp4_quant(x[0], ref.MX),
+           lambda: bn.bitnet_fp4_dequant(w, s, 300, ref.MX)]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail(f"call {i} was taken")
+    for dtype in (torch.float32,):  # types that the C entry refuses
+        with pytest.raises(bn.BitnetError):
+            bn.bitnet_fp4_linear(x, w, s, ref.MX, dtype=dtype)
+    with pytest.raises(bn.BitnetError):  # rows that overlap
+        bn.bitnet_fp4_quant(x[:1].expand(4, 256), ref.MX)
+    with pytest.raises(bn.BitnetError):  # 17 tokens need a workspace
+        bn.bitnet_fp4_linear(torch.zeros(17, 256, dtype=torch.bfloat16, device="cuda"), w, s, ref.MX,
+                             ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
