@@ -997,6 +997,19 @@ cudaError_t launch_pdl_cluster(Kern kern, unsigned grid, unsigned block, unsigne
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// Test hook: with BITNET_TEST_STALL=2 (few tokens) or 3 (more) the first such
+// product of the process leaves one wait to run out.
+bool fp4_test_stall(char kind) {
+    static std::atomic<int> armed{-1};
+    int a = armed.load(std::memory_order_relaxed);
+    if (a == -1) {
+        const char *e = getenv("BITNET_TEST_STALL");
+        const int v = e != nullptr && (e[0] == '2' || e[0] == '3') ? e[0] : 0;
+        if (armed.compare_exchange_strong(a, v)) a = v;
+    }
+    return a == kind && armed.compare_exchange_strong(a, 0);
+}
+
 bool fp4_code_map(CUtensorMap *m, const uint8_t *codes, int64_t rows, int64_t K, int box) {
     const uint64_t rb = (uint64_t)fp4_row_bytes(K);
     return encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, rb, (uint64_t)rows, rb, 128, (uint32_t)box,
@@ -1038,6 +1051,7 @@ int launch_fp4_small_variant(DeviceInfo *dev, const CUtensorMap &wmap, const CUt
 int launch_fp4_small(DeviceInfo *dev, const uint8_t *codes, int xtype, const uint8_t *w, int format, Fp4SmallArgs a,
                      cudaStream_t st) {
     a.split = fp4_split(a.N, a.K);
+    a.test_stall = fp4_test_stall('2');
     const int BT = a.M <= 16 ? 16 : (a.M <= 32 ? 32 : 64);
     CUtensorMap wmap, amap;
     memset(&amap, 0, sizeof(amap));
@@ -1116,6 +1130,7 @@ int launch_fp4_pair(DeviceInfo *dev, const uint8_t *codes, const uint8_t *sa, co
     a.tiles_m = (int)ceil_div(M, 256);
     a.tiles_n = (int)ceil_div(N, BT);
     a.vec = aligned(y, 16) && ldy % 8 == 0;
+    a.test_stall = fp4_test_stall('3');
     return fp4_by_format(format, [&](auto fm) {
         constexpr int F = decltype(fm)::value;
         switch (BT) {

@@ -122,6 +122,7 @@ struct Fp4SmallArgs {
     const float *ga, *gw;
     void *y;
     int split;               // CTAs per cluster
+    int test_stall;          // the first CTA never asks for its first stage (test of the bounded waits)
 };
 
 template <int FMT, int BT>
@@ -336,6 +337,7 @@ __global__ void __launch_bounds__(kFp4Threads, Fp4Small<FMT, BT>::kCtas)
         for (; i < n_i; ++i) {
             const int s = i % S, gi = i0 + i;
             if (i >= S && !warp_wait(&empty[s], (uint32_t)(i / S - 1) & 1u, abort_flag)) break;
+            if (a.test_stall && blockIdx.x == 0 && i == 0) continue;
             if (elect_one()) {
                 uint8_t *st = sm + s * L::kStage;
                 const uint32_t sb = scale_bytes(gi);

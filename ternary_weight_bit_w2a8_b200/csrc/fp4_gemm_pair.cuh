@@ -33,6 +33,7 @@ struct Fp4PairArgs {
     int ytype;
     int tiles_m, tiles_n;  // 256-token and BT-row tiles
     int vec;               // rows of y start on 16-byte boundaries
+    int test_stall;        // the first pair never asks for its first stage (test of the bounded waits)
 };
 
 template <int FMT, int BT>
@@ -293,6 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
                     ok = false;
                     break;
                 }
+                if (a.test_stall && pair == 0 && g == 0) continue;
                 if (elect_one()) {
                     uint8_t *st = sm + s * L::kStage;
                     const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
