@@ -3,7 +3,8 @@
 Argument marshalling only: every function takes torch CUDA tensors, passes
 their device pointers and the current CUDA stream to the C entry point of the
 same name (declared in include/bitnet_b200.h) and raises BitnetError on a
-non-zero status. All arithmetic runs in the library's CUDA kernels; there is
+non-zero status (the 4-bit functions through a native module, the others
+through ctypes). All arithmetic runs in the library's CUDA kernels; there is
 no CPU fallback. Importing the package does not load the library: the first
 call does, and raises if it has not been built.
 """
@@ -14,6 +15,7 @@ import os
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libbitnet_b200.so")
+BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
 
 BITNET_OK = 0
 BITNET_ERR_INVALID_ARG = 1
@@ -238,104 +240,31 @@ def bitnet_w2a8_gemm_noalloc(q, packed, N: int, y=None, stream=None):
 
 # ------------------------------------------------------------------ 4-bit floating point
 # The tensors of a call lie on one CUDA device, which need not be the current
-# one; x and y may be row-strided views, everything else is contiguous.  These
-# calls are short (a decode step is a few microseconds on the GPU), so the
-# checks avoid what costs the interpreter most: device objects, context
-# managers, size queries through ctypes and calls of their own (a call on ready
-# tensors spends 2 to 3 us here and 4 in the library and the launch).
+# one; x and y may be row-strided views, everything else is contiguous.  The
+# checks and the marshalling of these calls are native (csrc/binding.cpp).
 
-_torch = None
-_u8 = _f32 = _bf16 = None
-_dtypes = {}
-_current_device = _raw_stream = None
+_native = None
 
 
-def _load_torch():
-    global _torch, _u8, _f32, _bf16, _current_device, _raw_stream
+def _load_native():
+    """The native module (raises if it has not been built)."""
+    global _native
+    import torch  # noqa: F401  (its libraries are the module's)
+    lib()
+    if not os.path.exists(BINDING_PATH):
+        raise ImportError(f"{BINDING_PATH} is missing: build it with `python -m ternary_weight_bit_w2a8_b200.build`")
+    from . import _binding as module
+    module.set_error(BitnetError)
+    _native = module
+    return module
+
+
+def _on(stream, t):
+    """Makes `stream` current: what a call allocates belongs to the stream that it runs on."""
     import torch
-    _u8, _f32, _bf16 = torch.uint8, torch.float32, torch.bfloat16
-    _dtypes.update({torch.bfloat16: BITNET_BF16, torch.float16: BITNET_FP16, torch.float32: BITNET_FP32})
-    _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-    _torch = torch
-    return torch
-
-
-class _on:
-    """Makes device `index` and, where given, `stream` current: what a call
-    allocates belongs to the stream that it runs on."""
-
-    def __init__(self, index, stream):
-        if stream is not None and stream.device_index != index:
-            raise ValueError("stream must be one of the device that the tensors are on")
-        self.device = _torch.cuda.device(index)
-        self.stream = None if stream is None else _torch.cuda.stream(stream)
-
-    def __enter__(self):
-        self.device.__enter__()
-        if self.stream is not None:
-            self.stream.__enter__()
-
-    def __exit__(self, *exc):
-        if self.stream is not None:
-            self.stream.__exit__(*exc)
-        self.device.__exit__(*exc)
-
-
-def _device_of(t, name):
-    index = t.get_device()
-    if index < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return index
-
-
-def _float_type(dtype, name):
-    d = _dtypes.get(dtype)
-    if d is None:
-        raise ValueError(f"{name} must be bfloat16, float16 or float32, not {dtype}")
-    return d
-
-
-def _rows(t, name, index, shape=None):
-    """Row stride of a 2-D tensor whose rows are contiguous."""
-    if t.get_device() != index:
-        raise ValueError(f"{name} must be on the call's CUDA device")
-    size = t.shape
-    if len(size) != 2 or (size[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be 2-D with contiguous rows")
-    if shape is not None and size != shape:
-        raise ValueError(f"{name} must be {list(shape)}, not {list(size)}")
-    return t.stride(0) if size[0] > 1 else size[1]
-
-
-def _scalar(t, name, index):
-    """Pointer of a float32 tensor of one value (None for None)."""
-    if t is None:
-        return None
-    if t.dtype is not _f32 or t.get_device() != index or t.numel() < 1:
-        raise ValueError(f"{name} must be a float32 tensor of one value on the call's CUDA device")
-    return t.data_ptr()
-
-
-def _matrix(codes, scales, K, fmt, index, name):
-    """Pointers of a quantised matrix [rows, K], and its rows."""
-    size = codes.shape
-    if (len(size) != 2 or size[1] != (K + 127 >> 7) << 6 or codes.dtype is not _u8 or codes.get_device() != index
-            or not codes.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous uint8 tensor [rows, {(K + 127 >> 7) << 6}] for K = {K} on the "
-                         f"call's CUDA device, not {codes.dtype} {list(size)} on {codes.device}")
-    if (scales.dtype is not _u8 or scales.get_device() != index or not scales.is_contiguous()
-            or scales.numel() < _scale_bytes(size[0], K, fmt)):
-        raise ValueError(f"the scales of {name} must be a contiguous uint8 tensor of {_scale_bytes(size[0], K, fmt)} "
-                         f"bytes on the call's CUDA device, not {scales.dtype} {list(scales.shape)} on {scales.device}")
-    return codes.data_ptr(), scales.data_ptr(), size[0]
-
-
-def _scale_bytes(rows, K, fmt):
-    if fmt == BITNET_FP4_MX:
-        return (rows + 127 >> 7) * (K + 127 >> 7) << 9
-    if fmt == BITNET_FP4_NV:
-        return (rows + 127 >> 7) * (K + 127 >> 7) << 10
-    raise ValueError("fmt must be BITNET_FP4_MX or BITNET_FP4_NV")
+    if stream.device_index != t.get_device():
+        raise ValueError("stream must be one of the device that the tensors are on")
+    return torch.cuda.stream(stream)
 
 
 def bitnet_fp4_code_bytes(rows: int, K: int) -> int:
@@ -361,120 +290,47 @@ def bitnet_fp4_workspace_bytes(M: int, N: int, K: int, fmt: int) -> int:
 
 def bitnet_fp4_tensor_scale(x, g=None, stream=None):
     """Tensor scale of the NV format, max|x| / 2688 over the finite values of x -> float32 tensor [1]."""
-    if _torch is None:
-        _load_torch()
-    index = _device_of(x, "x")
-    if stream is not None or index != _current_device():
-        with _on(index, stream):
-            return bitnet_fp4_tensor_scale(x, g)
-    ldx = _rows(x, "x", index)
-    rows, K = x.shape
-    if g is None:
-        g = x.new_empty(1, dtype=_f32)
-    rc = lib().bitnet_fp4_tensor_scale(x.data_ptr(), _float_type(x.dtype, "x"), rows, K, ldx, _scalar(g, "g", index),
-                                       _raw_stream(index))
-    if rc:
-        raise BitnetError(rc, "bitnet_fp4_tensor_scale")
-    return g
+    native = _native or _load_native()
+    if stream is not None:
+        with _on(stream, x):
+            return native.tensor_scale(x, g)
+    return native.tensor_scale(x, g)
 
 
 def bitnet_fp4_quant(x, fmt: int, g=None, codes=None, scales=None, stream=None):
     """Quantises x [rows, K] -> (codes uint8 [rows, K_pad / 2], scales uint8 [bitnet_fp4_scale_bytes(rows, K, fmt)])."""
-    if _torch is None:
-        _load_torch()
-    index = _device_of(x, "x")
-    if stream is not None or index != _current_device():
-        with _on(index, stream):
-            return bitnet_fp4_quant(x, fmt, g, codes, scales)
-    ldx = _rows(x, "x", index)
-    rows, K = x.shape
-    if codes is None and scales is None:
-        codes = x.new_empty((rows, (K + 127 >> 7) << 6), dtype=_u8)
-        scales = codes.new_empty(_scale_bytes(rows, K, fmt))
-        cp, sp = codes.data_ptr(), scales.data_ptr()
-    else:
-        if codes is None or scales is None:
-            raise ValueError("codes and scales are given together")
-        cp, sp, n = _matrix(codes, scales, K, fmt, index, "codes")
-        if n != rows:
-            raise ValueError("codes and x differ in their rows")
-    rc = lib().bitnet_fp4_quant(x.data_ptr(), _float_type(x.dtype, "x"), rows, K, ldx, fmt, _scalar(g, "g", index), cp,
-                                sp, _raw_stream(index))
-    if rc:
-        raise BitnetError(rc, "bitnet_fp4_quant")
-    return codes, scales
+    native = _native or _load_native()
+    if stream is not None:
+        with _on(stream, x):
+            return native.quant(x, fmt, g, codes, scales)
+    return native.quant(x, fmt, g, codes, scales)
 
 
 def bitnet_fp4_dequant(codes, scales, K: int, fmt: int, g=None, dtype=None, y=None, stream=None):
     """The values of a quantised matrix -> y [rows, K] (bfloat16 unless dtype or y says otherwise)."""
-    if _torch is None:
-        _load_torch()
-    index = _device_of(codes, "codes")
-    if stream is not None or index != _current_device():
-        with _on(index, stream):
-            return bitnet_fp4_dequant(codes, scales, K, fmt, g, dtype, y)
-    cp, sp, rows = _matrix(codes, scales, K, fmt, index, "codes")
-    if y is None:
-        y, ldy = codes.new_empty((rows, K), dtype=dtype or _bf16), K
-    else:
-        ldy = _rows(y, "y", index, (rows, K))
-    rc = lib().bitnet_fp4_dequant(cp, sp, rows, K, fmt, _scalar(g, "g", index), y.data_ptr(),
-                                  _float_type(y.dtype, "y"), ldy, _raw_stream(index))
-    if rc:
-        raise BitnetError(rc, "bitnet_fp4_dequant")
-    return y
+    native = _native or _load_native()
+    if stream is not None:
+        with _on(stream, codes):
+            return native.dequant(codes, scales, K, fmt, g, dtype, y)
+    return native.dequant(codes, scales, K, fmt, g, dtype, y)
 
 
 def bitnet_fp4_gemm(a, a_scales, w, w_scales, K: int, fmt: int, ga=None, gw=None, dtype=None, y=None, stream=None):
     """y = A W^T of quantised A [M, K] and W [N, K] -> [M, N] (bfloat16 or float16)."""
-    if _torch is None:
-        _load_torch()
-    index = _device_of(a, "a")
-    if stream is not None or index != _current_device():
-        with _on(index, stream):
-            return bitnet_fp4_gemm(a, a_scales, w, w_scales, K, fmt, ga, gw, dtype, y)
-    ap, asp, M = _matrix(a, a_scales, K, fmt, index, "a")
-    wp, wsp, N = _matrix(w, w_scales, K, fmt, index, "w")
-    if y is None:
-        y, ldy = a.new_empty((M, N), dtype=dtype or _bf16), N
-    else:
-        ldy = _rows(y, "y", index, (M, N))
-    rc = lib().bitnet_fp4_gemm(ap, asp, _scalar(ga, "ga", index), wp, wsp, _scalar(gw, "gw", index), fmt, y.data_ptr(),
-                               _float_type(y.dtype, "y"), M, N, K, ldy, _raw_stream(index))
-    if rc:
-        raise BitnetError(rc, "bitnet_fp4_gemm")
-    return y
+    native = _native or _load_native()
+    if stream is not None:
+        with _on(stream, a):
+            return native.gemm(a, a_scales, w, w_scales, K, fmt, ga, gw, dtype, y)
+    return native.gemm(a, a_scales, w, w_scales, K, fmt, ga, gw, dtype, y)
 
 
 def bitnet_fp4_linear(x, w, w_scales, fmt: int, ga=None, gw=None, dtype=None, y=None, ws=None, stream=None):
     """y = quantised(x) W^T: x [M, K] of any type, quantised W [N, K] -> [M, N] (bfloat16 or float16)."""
-    if _torch is None:
-        _load_torch()
-    index = _device_of(x, "x")
-    if stream is not None or index != _current_device():
-        with _on(index, stream):
-            return bitnet_fp4_linear(x, w, w_scales, fmt, ga, gw, dtype, y, ws)
-    ldx = _rows(x, "x", index)
-    M, K = x.shape
-    wp, wsp, N = _matrix(w, w_scales, K, fmt, index, "w")
-    if y is None:
-        y, ldy = x.new_empty((M, N), dtype=dtype or _bf16), N
-    else:
-        ldy = _rows(y, "y", index, (M, N))
-    wsb = 0
-    if ws is not None:
-        if ws.dtype is not _u8 or ws.get_device() != index or not ws.is_contiguous():
-            raise ValueError("ws must be a contiguous uint8 tensor on the call's CUDA device")
-        wsb = ws.numel()
-    elif M > 16:  # fewer tokens need none
-        wsb = bitnet_fp4_workspace_bytes(M, N, K, fmt)
-        ws = x.new_empty(wsb, dtype=_u8)
-    rc = lib().bitnet_fp4_linear(x.data_ptr(), _float_type(x.dtype, "x"), ldx, _scalar(ga, "ga", index), wp, wsp,
-                                 _scalar(gw, "gw", index), fmt, y.data_ptr(), _float_type(y.dtype, "y"), M, N, K, ldy,
-                                 None if ws is None else ws.data_ptr(), wsb, _raw_stream(index))
-    if rc:
-        raise BitnetError(rc, "bitnet_fp4_linear")
-    return y
+    native = _native or _load_native()
+    if stream is not None:
+        with _on(stream, x):
+            return native.linear(x, w, w_scales, fmt, ga, gw, dtype, y, ws)
+    return native.linear(x, w, w_scales, fmt, ga, gw, dtype, y, ws)
 
 
 def bitnet_get_device_error(stream=None) -> int:
