@@ -946,8 +946,16 @@ int fp4_by_format(int format, F f) {
     return f(std::integral_constant<int, BITNET_FP4_NV>{});
 }
 
-inline int64_t fp4_patches(int64_t rows, int64_t K) {
-    return ceil_div(rows, kFp4TileRows) * ceil_div(k_pad(K), kFp4PatchK);
+// Patches of `r` rows x 256 k in the 128-row bands of a matrix, and the rows
+// that a launch takes: 32 where patches of 64 are fewer than four per SM.
+inline int64_t fp4_patches(int64_t rows, int64_t K, int r) {
+    return ceil_div(rows, kFp4TileRows) * (kFp4TileRows / r) * ceil_div(k_pad(K), kFp4PatchK);
+}
+inline int fp4_patch_rows(int64_t rows, int64_t K) { return fp4_patches(rows, K, 64) < 4 * 148 ? 32 : 64; }
+template <typename F>
+int fp4_by_rows(int64_t rows, int64_t K, F f) {
+    if (fp4_patch_rows(rows, K) == 32) return f(std::integral_constant<int, 32>{});
+    return f(std::integral_constant<int, 64>{});
 }
 
 // Whether rows of `esize`-byte elements start on 16-byte boundaries.
@@ -958,11 +966,13 @@ int launch_fp4_quant(const void *x, int dtype, int64_t rows, int64_t K, int64_t 
     const bool al = fp4_rows_aligned(x, ldx, fp4_dtype_size(dtype));
     return fp4_by_type(dtype, [&](auto dt) {
         return fp4_by_format(format, [&](auto fm) {
-            constexpr int D = decltype(dt)::value, F = decltype(fm)::value;
-            using T = typename Fp4Type<D>::T;
-            return launched(launch_pdl(al ? fp4_quant_kernel<D, F, true> : fp4_quant_kernel<D, F, false>,
-                                       dim3((unsigned)fp4_patches(rows, K)), dim3(kThreads), (size_t)0, st,
-                                       static_cast<const T *>(x), rows, K, ldx, g, codes, scales));
+            return fp4_by_rows(rows, K, [&](auto rw) {
+                constexpr int D = decltype(dt)::value, F = decltype(fm)::value, R = decltype(rw)::value;
+                using T = typename Fp4Type<D>::T;
+                return launched(launch_pdl(al ? fp4_quant_kernel<D, F, true, R> : fp4_quant_kernel<D, F, false, R>,
+                                           dim3((unsigned)fp4_patches(rows, K, R)), dim3(kThreads), (size_t)0, st,
+                                           static_cast<const T *>(x), rows, K, ldx, g, codes, scales));
+            });
         });
     });
 }
@@ -1424,7 +1434,7 @@ BITNET_API int bitnet_fp4_quant(const void *x, int dtype, int64_t rows, int64_t 
     if (x == nullptr || codes == nullptr || scales == nullptr) return BITNET_ERR_INVALID_ARG;
     if (!aligned(x, fp4_dtype_size(dtype)) || !aligned(g, 4) || !aligned(codes, 16) || !aligned(scales, 16))
         return BITNET_ERR_ALIGNMENT;
-    if (fp4_patches(rows, K) > (1LL << 31) - 1) return BITNET_ERR_UNSUPPORTED;
+    if (fp4_patches(rows, K, 64) > (1LL << 31) - 1) return BITNET_ERR_UNSUPPORTED;
     DeviceInfo *dev = nullptr;
     const int rc = device_info(&dev);
     if (rc != BITNET_OK) return rc;
@@ -1439,19 +1449,21 @@ BITNET_API int bitnet_fp4_dequant(const uint8_t *codes, const uint8_t *scales, i
     if (y == nullptr || codes == nullptr || scales == nullptr) return BITNET_ERR_INVALID_ARG;
     if (!aligned(y, fp4_dtype_size(dtype)) || !aligned(g, 4) || !aligned(codes, 16) || !aligned(scales, 16))
         return BITNET_ERR_ALIGNMENT;
-    if (fp4_patches(rows, K) > (1LL << 31) - 1) return BITNET_ERR_UNSUPPORTED;
+    if (fp4_patches(rows, K, 64) > (1LL << 31) - 1) return BITNET_ERR_UNSUPPORTED;
     DeviceInfo *dev = nullptr;
     const int rc = device_info(&dev);
     if (rc != BITNET_OK) return rc;
     const bool al = fp4_rows_aligned(y, ldy, fp4_dtype_size(dtype));
     return fp4_by_type(dtype, [&](auto dt) {
         return fp4_by_format(format, [&](auto fm) {
-            constexpr int D = decltype(dt)::value, F = decltype(fm)::value;
-            using T = typename Fp4Type<D>::T;
-            return launched(launch_pdl(al ? fp4_dequant_kernel<D, F, true> : fp4_dequant_kernel<D, F, false>,
-                                       dim3((unsigned)fp4_patches(rows, K)), dim3(kThreads), (size_t)0,
-                                       static_cast<cudaStream_t>(stream), codes, scales, rows, K, g,
-                                       static_cast<T *>(y), ldy));
+            return fp4_by_rows(rows, K, [&](auto rw) {
+                constexpr int D = decltype(dt)::value, F = decltype(fm)::value, R = decltype(rw)::value;
+                using T = typename Fp4Type<D>::T;
+                return launched(launch_pdl(al ? fp4_dequant_kernel<D, F, true, R> : fp4_dequant_kernel<D, F, false, R>,
+                                           dim3((unsigned)fp4_patches(rows, K, R)), dim3(kThreads), (size_t)0,
+                                           static_cast<cudaStream_t>(stream), codes, scales, rows, K, g,
+                                           static_cast<T *>(y), ldy));
+            });
         });
     });
 }
@@ -1501,7 +1513,7 @@ BITNET_API int bitnet_fp4_linear(const void *x, int xdtype, int64_t ldx, const f
     const int64_t need = M > kFp4FusedTokens && K > 0 ? cb + bitnet_fp4_scale_bytes(M, K, format) : 0;
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return BITNET_ERR_WORKSPACE;
     if (need > 0 && !aligned(workspace, 256)) return BITNET_ERR_ALIGNMENT;
-    if (fp4_patches(M, K) > (1LL << 31) - 1) return BITNET_ERR_UNSUPPORTED;
+    if (fp4_patches(M, K, 64) > (1LL << 31) - 1) return BITNET_ERR_UNSUPPORTED;
     DeviceInfo *dev = nullptr;
     int rc = device_info(&dev);
     if (rc != BITNET_OK) return rc;

@@ -253,20 +253,22 @@ __device__ __forceinline__ uint32_t fp4_codes8(const uint64_t (&x)[4], float inv
 }
 
 // ------------------------------------------------------------------ quantisation
-// A CTA quantises a patch of 128 rows x 256 k, so that it writes whole scale
-// tiles.  A lane takes 32 bytes of a row (16 values, 8 of fp32): one block of
-// NV, half of one of MX, or half and a quarter; the lanes of a block share its
-// maximum by shuffles.  A lane asks for four rows before it uses the first
-// (128 bytes in flight: 13824 x 5120 bf16 into NV takes 39 us, one row at a
-// time 53).  Scale bytes are put together in shared memory; the rows of the
-// last band past the matrix get scale 0.  The CTAs start at the matrix's end:
-// where the tensor scale has just read it, that is what L2 still holds (2 % for
-// 13824 x 5120).
+// A CTA quantises a patch of ROWS rows x 256 k.  A lane takes 32 bytes of a row
+// (16 values, 8 of fp32): one block of NV, half of one of MX, or half and a
+// quarter; the lanes of a block share its maximum by shuffles.  A lane asks for
+// up to four rows before it uses the first (13824 x 5120 bf16 into NV: 33 us,
+// one row at a time 53; packed fp32 arithmetic is 3 of what is between).  Scale
+// bytes are put together in shared memory, so that words of four go out; rows
+// of the last band past the matrix get scale 0.  The CTAs start at the matrix's
+// end: where the tensor scale has just read it, that is what L2 still holds
+// (2 % for 13824 x 5120).  Patches of 32 rows where 64 would leave SMs idle:
+// 997 x 6910 fp16 takes 6.6 us with 32, 7.5 with 64, 10.1 with 128, 13824 x
+// 5120 bf16 36.3, 34.1 and 36.1.
 //   ALIGNED: rows of x start on 16-byte boundaries.  Otherwise a warp reads a
 // row's values in order, one to a lane, and shared memory turns them round.
 constexpr int kFp4PatchK = 256;
 
-template <int DT, int FMT, bool ALIGNED>
+template <int DT, int FMT, bool ALIGNED, int ROWS>
 __global__ void __launch_bounds__(kThreads) fp4_quant_kernel(const typename Fp4Type<DT>::T *__restrict__ x,
                                                              int64_t rows, int64_t K, int64_t ldx,
                                                              const float *__restrict__ g, uint8_t *__restrict__ codes,
@@ -277,26 +279,29 @@ __global__ void __launch_bounds__(kThreads) fp4_quant_kernel(const typename Fp4T
     constexpr int kLanes = kFp4PatchK / V;        // lanes of a row: 16 or 32
     constexpr int kTiles = kFp4PatchK / (4 * B);  // scale tiles of a patch: 2 or 4
     constexpr int kStep = kThreads / kLanes;      // rows that the CTA takes at once
-    constexpr int kAhead = ALIGNED ? 4 : 2;
-    __shared__ alignas(16) uint8_t st[kTiles * kFp4TileBytes];
+    constexpr int kMost = ALIGNED ? 4 : 2, kAhead = ROWS / kStep < kMost ? ROWS / kStep : kMost;
+    constexpr int kParts = kFp4TileRows / ROWS;   // patches of a 128-row band
+    constexpr int kWords = ROWS / 32;             // 4-byte words of a tile's 16-byte row that a patch fills
+    static_assert(ROWS == 32 || ROWS == 64, "rows of a patch");
+    __shared__ uint32_t st[kTiles * 32 * kWords];
     __shared__ alignas(16) T turn[ALIGNED ? 1 : kStep * kFp4PatchK];
     const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
     const int64_t patches_k = ceil_div(k_pad(K), kFp4PatchK);
-    const int64_t block = gridDim.x - 1 - blockIdx.x, band = block / patches_k, pk = block % patches_k;
+    const int64_t block = gridDim.x - 1 - blockIdx.x, part = block / patches_k, pk = block % patches_k;
     const int64_t row_bytes = fp4_row_bytes(K), tiles = fp4_scale_tiles(K, FMT);
     const int64_t k = pk * kFp4PatchK + V * lane;
     const bool wide = ((reinterpret_cast<uintptr_t>(x) | (uintptr_t)(ldx * (int64_t)sizeof(T))) & 31) == 0;
-    const int64_t left = rows - band * kFp4TileRows;
-    const int nrows = (int)(left < kFp4TileRows ? left : kFp4TileRows);
-    if (nrows < kFp4TileRows)
-        for (int i = threadIdx.x; i < kTiles * kFp4TileBytes / 4; i += kThreads) reinterpret_cast<uint32_t *>(st)[i] = 0;
+    const int64_t left = rows - part * ROWS;
+    const int nrows = (int)(left < 0 ? 0 : (left < ROWS ? left : ROWS));
+    if (nrows < ROWS)
+        for (int i = threadIdx.x; i < kTiles * 32 * kWords; i += kThreads) st[i] = 0;
     pdl_wait();
     pdl_launch_dependents();
     const float inv = g != nullptr ? __frcp_rn(*g) : 1.0f;
     __syncthreads();
-    x += band * kFp4TileRows * ldx;
-    codes += band * kFp4TileRows * row_bytes + k / 2;
-    const int at = (lane * V / (4 * B)) * kFp4TileBytes + (lane * V / B & 3);
+    x += part * ROWS * ldx;
+    codes += part * ROWS * row_bytes + k / 2;
+    const int at = (lane * V / (4 * B)) * 32 * kWords * 4 + (lane * V / B & 3);
     const bool stored = k / 2 < row_bytes;
     for (int r0 = group; r0 - group < nrows; r0 += kAhead * kStep) {  // (whole warps go on: they shuffle)
         Fp4Raw<DT> v[kAhead];
@@ -352,15 +357,21 @@ __global__ void __launch_bounds__(kThreads) fp4_quant_kernel(const typename Fp4T
                 else
                     *reinterpret_cast<uint32_t *>(codes + r * row_bytes) = c[0];
             }
-            if (lane % (B / V) == 0) st[at + 16 * (r & 31) + 4 * (r >> 5)] = (uint8_t)q.byte;
+            if (lane % (B / V) == 0)
+                reinterpret_cast<uint8_t *>(st)[at + ((r & 31) * kWords + (r >> 5)) * 4] = (uint8_t)q.byte;
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < kTiles * kFp4TileBytes / 16; i += kThreads) {
-        const int64_t t = pk * kTiles + i / (kFp4TileBytes / 16);
-        if (t < tiles)
-            reinterpret_cast<uint4 *>(scales + (band * tiles + t) * kFp4TileBytes)[i % (kFp4TileBytes / 16)] =
-                reinterpret_cast<const uint4 *>(st)[i];
+    // word w of tile row r of a tile: rows r + 32 w of the patch
+    uint32_t *to = reinterpret_cast<uint32_t *>(scales + part / kParts * tiles * kFp4TileBytes) + part % kParts * kWords;
+    for (int i = threadIdx.x; i < kTiles * 32; i += kThreads) {
+        const int64_t t = pk * kTiles + i / 32;
+        if (t >= tiles) continue;
+        uint32_t *p = to + t * (kFp4TileBytes / 4) + (i & 31) * 4;
+        if constexpr (kWords == 2)
+            *reinterpret_cast<uint2 *>(p) = make_uint2(st[i * 2], st[i * 2 + 1]);
+        else
+            *p = st[i];
     }
 }
 
@@ -396,36 +407,37 @@ __device__ __forceinline__ uint32_t fp4_round2(float2 v) {
     return r;
 }
 
-// A CTA reads a patch of 128 rows x 256 k; a lane takes 32 bytes of a row of y
+// A CTA reads a patch of ROWS rows x 256 k; a lane takes 32 bytes of a row of y
 // (16 values from 8 code bytes, 8 of fp32 from 4).  ALIGNED (rows of y start on
 // 16-byte boundaries): stored as they are, at once where they start on a
 // 32-byte boundary.  Otherwise the lanes of a row put them down in shared
 // memory as 4-byte words that lie on 4-byte boundaries of y (shifted by one
 // value where the row starts between two) and store those in order: 997 x 6910
 // fp16 took 22 us with lanes that stored their own pairs.
-template <int DT, int FMT, bool ALIGNED>
+template <int DT, int FMT, bool ALIGNED, int ROWS>
 __global__ void __launch_bounds__(kThreads) fp4_dequant_kernel(const uint8_t *__restrict__ codes,
                                                                const uint8_t *__restrict__ scales, int64_t rows,
                                                                int64_t K, const float *__restrict__ g,
                                                                typename Fp4Type<DT>::T *__restrict__ y, int64_t ldy) {
     using T = typename Fp4Type<DT>::T;
     constexpr int B = FMT == BITNET_FP4_MX ? 32 : 16;
-    constexpr int V = Fp4Raw<DT>::kValues, kLanes = kFp4PatchK / V, kStep = kThreads / kLanes, kAhead = 4;
+    constexpr int V = Fp4Raw<DT>::kValues, kLanes = kFp4PatchK / V, kStep = kThreads / kLanes;
+    constexpr int kAhead = ROWS / kStep < 4 ? ROWS / kStep : 4, kParts = kFp4TileRows / ROWS;
     constexpr int kRowWords = 8 * kLanes + kLanes;  // a word of padding after 8: lanes 8 words apart share no banks
     __shared__ uint32_t turn[ALIGNED ? 1 : kStep * kRowWords];
     const int64_t patches_k = ceil_div(k_pad(K), kFp4PatchK);
-    const int64_t band = (int64_t)blockIdx.x / patches_k, pk = (int64_t)blockIdx.x % patches_k;
+    const int64_t part = (int64_t)blockIdx.x / patches_k, pk = (int64_t)blockIdx.x % patches_k;
     const int64_t row_bytes = fp4_row_bytes(K), tiles = fp4_scale_tiles(K, FMT), k0 = pk * kFp4PatchK;
-    const int64_t left = rows - band * kFp4TileRows;
-    const int nrows = (int)(left < kFp4TileRows ? left : kFp4TileRows);
+    const int64_t left = rows - part * ROWS;
+    const int nrows = (int)(left < 0 ? 0 : (left < ROWS ? left : ROWS));
     const bool wide = ((reinterpret_cast<uintptr_t>(y) | (uintptr_t)(ldy * (int64_t)sizeof(T))) & 31) == 0;
     const int group = threadIdx.x / kLanes, lane = threadIdx.x % kLanes, k = V * lane;
     pdl_wait();
     pdl_launch_dependents();
     const float gs = g != nullptr ? *g : 1.0f;
-    codes += band * kFp4TileRows * row_bytes + (k0 + k) / 2;
-    scales += (band * tiles + (k0 + k) / (4 * B)) * kFp4TileBytes + (k / B & 3);
-    y += band * kFp4TileRows * ldy + k0;
+    codes += part * ROWS * row_bytes + (k0 + k) / 2;
+    scales += (part / kParts * tiles + (k0 + k) / (4 * B)) * kFp4TileBytes + part % kParts * (ROWS / 32 * 4) + (k / B & 3);
+    y += part * ROWS * ldy + k0;
     const int cols = (int)(K - k0 < kFp4PatchK ? K - k0 : kFp4PatchK);
     uint32_t *words = turn + group * kRowWords;
     for (int r0 = group; r0 - group < nrows; r0 += kAhead * kStep) {  // (whole warps go on: they shuffle)
