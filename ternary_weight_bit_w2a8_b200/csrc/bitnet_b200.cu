@@ -1027,21 +1027,23 @@ bool fp4_code_map(CUtensorMap *m, const uint8_t *codes, int64_t rows, int64_t K,
 }
 
 // Tokens that the small kernel takes; more go to the pair kernel.
-// (64 x 5120 x 5120 takes 8.2 us in the small kernel, 9.1 in the other; 128 x
-// 13824 x 2560 11.2 and 8.7).
+// (64 x 2560 x 6912 takes 6.8 us in the small kernel, 9.0 in the other, 64 x
+// 27648 x 5120 15.2 and 18.3; 128 x 13824 x 2560 10.6 and 8.0).
 constexpr int kFp4SmallTokens = 64;
 
-// CTAs per weight tile of the small kernel: as many as leave 240 CTAs or fewer
-// (a CTA lives some 3 us beside its loads, so more of them than the SMs hold at
-// once cost more than the shorter ranges of k save) and two stages to each.
+// CTAs per weight tile of the small kernel: as many as leave 240 CTAs or fewer,
+// 150 from 17 tokens up (a CTA lives some 3 us beside its loads, so more of
+// them than the SMs hold at once cost more than the shorter ranges of k save)
+// and two stages to each.
 // Measured, in us, for 1, 2, 4 and 8: 1 x 2560 x 6912 10.9, 7.4, 5.5, 5.1;
 // 1 x 6912 x 2560 5.3, 5.2, 4.6, 8.1; 1 x 13824 x 5120 10.1, 9.5, 11.8, 14.9;
-// 1 x 55296 x 5120 23.2, 26.7, 34.4, 48.4.  From the sizes alone, so that the
+// 1 x 55296 x 5120 23.2, 26.7, 34.4, 48.4; 33 x 3200 x 4800 8.1, 6.5, 5.6, 6.1;
+// 64 x 13824 x 2560 7.7, 8.5, 13.4, 25.8.  From the sizes alone, so that the
 // sums' grouping depends on nothing else.
-int fp4_split(int64_t N, int64_t K) {
-    const int64_t tiles = ceil_div(N, kFp4Rows), nk = ceil_div(k_pad(K), kFp4StageK);
+int fp4_split(int64_t M, int64_t N, int64_t K) {
+    const int64_t tiles = ceil_div(N, kFp4Rows), nk = ceil_div(k_pad(K), kFp4StageK), most = M <= 16 ? 240 : 150;
     int s = 1;
-    while (2 * s <= kFp4MaxSplit && tiles * 2 * s <= 240 && nk >= 4 * s) s *= 2;
+    while (2 * s <= kFp4MaxSplit && tiles * 2 * s <= most && nk >= 4 * s) s *= 2;
     return s;
 }
 
@@ -1060,7 +1062,7 @@ int launch_fp4_small_variant(DeviceInfo *dev, const CUtensorMap &wmap, const CUt
 // codes == null: the tokens are quantised in the kernel (a.x, of type xtype).
 int launch_fp4_small(DeviceInfo *dev, const uint8_t *codes, int xtype, const uint8_t *w, int format, Fp4SmallArgs a,
                      cudaStream_t st) {
-    a.split = fp4_split(a.N, a.K);
+    a.split = fp4_split(a.M, a.N, a.K);
     a.test_stall = fp4_test_stall('2');
     const int BT = a.M <= 16 ? 16 : (a.M <= 32 ? 32 : 64);
     CUtensorMap wmap, amap;
@@ -1415,7 +1417,7 @@ BITNET_API int bitnet_fp4_tensor_scale(const void *x, int dtype, int64_t rows, i
         constexpr int D = decltype(dt)::value;
         using T = typename Fp4Type<D>::T;
         int64_t blocks = ceil_div(rows * ceil_div(K, kFp4ScalePiece<D>), kThreads / 32);
-        if (blocks > 8 * dev->sm_count) blocks = 8 * dev->sm_count;
+        if (blocks > 4 * dev->sm_count) blocks = 4 * dev->sm_count;  // one wave: as many as fit
         if (blocks < 1) blocks = 1;
         if (blocks > 1) {
             const int rc1 = launched(launch_pdl(fp4_clear_kernel, dim3(1), dim3(1), (size_t)0, st, g));

@@ -541,7 +541,7 @@ template <int DT>
 constexpr int kFp4ScalePiece = Fp4Raw<DT>::kValues * 32 * kFp4ScaleLoads;
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads) fp4_tensor_scale_kernel(const typename Fp4Type<DT>::T *__restrict__ x,
+__global__ void __launch_bounds__(kThreads, 4) fp4_tensor_scale_kernel(const typename Fp4Type<DT>::T *__restrict__ x,
                                                                     int64_t rows, int64_t K, int64_t ldx, float *g) {
     using T = typename Fp4Type<DT>::T;
     constexpr int V = Fp4Raw<DT>::kValues;

@@ -200,27 +200,29 @@ __device__ __forceinline__ void store_box(const Fp4PairArgs &a, uint8_t *box, co
     // by one, a store holds up the next row's reads).
     const int width = 8 * pieces, last = width / 2 - 1;
     const int cols = (int)(a.N - nb < width ? a.N - nb : width);
-    auto value = [&](int r, int e) -> uint32_t {
-        return *reinterpret_cast<const uint16_t *>(box + r * 128 + (((e >> 3) ^ (r & 7)) << 4) + 2 * (e & 7));
-    };
-    const uintptr_t y0 = reinterpret_cast<uintptr_t>(y + nb) >> 1;
-    for (int r0 = 0; r0 < rows && lane <= last; r0 += 8) {
+    if (lane > last || cols <= 0) return;
+    // rows of a batch start in the middle of a word, or do not, like row i of the first (batches are eight rows)
+    const int first_odd = (int)(reinterpret_cast<uintptr_t>(y + nb) >> 1 & 1), step_odd = (int)(a.ldy & 1);
+    uint16_t *yr = y + nb;
+    for (int r0 = 0; r0 < rows; r0 += 8, yr += 8 * a.ldy) {
         uint32_t pr[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int e = 2 * lane + (int)((y0 + (r0 + i) * a.ldy) & 1);
-            pr[i] = value(r0 + i, e) | value(r0 + i, (e + 1) & (width - 1)) << 16;
+            const int e = 2 * lane + ((first_odd + i * step_odd) & 1), f = (e + 1) & (width - 1);
+            const uint8_t *br = box + r0 * 128 + i * 128;
+            pr[i] = *reinterpret_cast<const uint16_t *>(br + (((e >> 3) ^ i) << 4) + 2 * (e & 7)) |
+                    (uint32_t) * reinterpret_cast<const uint16_t *>(br + (((f >> 3) ^ i) << 4) + 2 * (f & 7)) << 16;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (r0 + i >= rows) break;
-            uint16_t *yr = y + (r0 + i) * a.ldy + nb;
-            const int odd = (int)((y0 + (r0 + i) * a.ldy) & 1), e = 2 * lane + odd;
+            const int odd = (first_odd + i * step_odd) & 1, e = 2 * lane + odd;
+            uint16_t *p = yr + i * a.ldy;
             if (e + 1 < cols)
-                *reinterpret_cast<uint32_t *>(yr + e) = pr[i];
+                *reinterpret_cast<uint32_t *>(p + e) = pr[i];
             else if (e < cols)
-                yr[e] = (uint16_t)pr[i];
-            if (odd && lane == last && cols > 0) yr[0] = (uint16_t)(pr[i] >> 16);
+                p[e] = (uint16_t)pr[i];
+            if (odd && lane == last) p[0] = (uint16_t)(pr[i] >> 16);
         }
     }
 }
