@@ -1123,7 +1123,8 @@ int launch_fp4_pair(DeviceInfo *dev, const uint8_t *codes, const uint8_t *sa, co
     const int BT = fp4_pair_width(M, N, K, format);
     if (ceil_div(M, 256) * ceil_div(N, BT) > (int64_t)1 << 30) return BITNET_ERR_UNSUPPORTED;
     const int64_t tiles = fp4_scale_tiles(K, format);
-    if ((ceil_div(M, 128) + 1) * tiles > INT32_MAX || (ceil_div(N, 128) + 1) * tiles > INT32_MAX || N > INT32_MAX)
+    if ((ceil_div(M, 128) + 1) * tiles > INT32_MAX || (ceil_div(N, 128) + 3) * tiles > INT32_MAX ||
+        M > INT32_MAX - 256 || N > INT32_MAX - 384)
         return BITNET_ERR_UNSUPPORTED;  // TMA coordinates
     CUtensorMap amap, wmap, samap, swmap;
     auto scale_map = [&](CUtensorMap *m, const uint8_t *s, int64_t rows) {

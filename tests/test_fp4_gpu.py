@@ -375,3 +375,41 @@ def test_binding_refuses_what_does_not_fit():
     with pytest.raises(bn.BitnetError):  # 17 tokens need a workspace
         bn.bitnet_fp4_linear(torch.zeros(17, 256, dtype=torch.bfloat16, device="cuda"), w, s, ref.MX,
                              ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+def test_offsets_beyond_32_bits():
+    """Codes of 4.5 GB, an activation matrix of 2.2 and a product of 2.8 thousand million elements: their last rows."""
+    fmt, gen = ref.NV, torch.Generator(device="cuda").manual_seed(1)
+    N, K = 70000, 131072
+    w = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda", generator=gen)
+    s = torch.randint(52, 60, (bn.bitnet_fp4_scale_bytes(N, K, fmt),), dtype=torch.uint8, device="cuda", generator=gen)
+    last = N // 128 * 128
+    wv = bn.bitnet_fp4_dequant(w[last:], s[bn.bitnet_fp4_scale_bytes(last, K, fmt):], K, fmt, dtype=torch.float32).double()
+    gw = torch.tensor([2.0 ** -12], device="cuda")
+    for M in (1, 70):
+        x = torch.randn(M, K, device="cuda", generator=gen)
+        a, a_s = bn.bitnet_fp4_quant(x, fmt)
+        av = bn.bitnet_fp4_dequant(a, a_s, K, fmt, dtype=torch.float32).double()
+        y = bn.bitnet_fp4_gemm(a, a_s, w, s, K, fmt, gw=gw)[:, last:].double()
+        want, mag = av @ wv.t() * 2.0 ** -12, av.abs() @ wv.abs().t() * 2.0 ** -12
+        assert bool(((y - want).abs() <= want.abs() * 2.0 ** -8 + mag * (K / 16 + 16) * 2.0 ** -22).all())
+    del w, s, wv
+    rows, K = 33000, 65600
+    x = torch.randn(rows, K, device="cuda", generator=gen).to(torch.bfloat16)
+    codes, scales = bn.bitnet_fp4_quant(x, fmt)
+    c, sb = ref.quantise(x[-8:].float().cpu().numpy(), fmt)
+    p, _ = ref.pack(c, sb, fmt)
+    got = codes[-8:].cpu().numpy()
+    assert np.array_equal(got & 0x77, p & 0x77)
+    y = bn.bitnet_fp4_dequant(codes, scales, K, fmt)
+    assert np.array_equal(y[-8:].float().cpu().numpy(),
+                          torch.from_numpy(ref.values(c, sb, fmt)[:, :K]).to(torch.bfloat16).float().numpy())
+    del x, codes, scales, y
+    M, N, K = 70000, 40000, 128
+    a, a_s = bn.bitnet_fp4_quant(torch.randn(M, K, device="cuda", generator=gen), fmt)
+    w, w_s = bn.bitnet_fp4_quant(torch.randn(N, K, device="cuda", generator=gen), fmt)
+    y = bn.bitnet_fp4_gemm(a, a_s, w, w_s, K, fmt)
+    av = bn.bitnet_fp4_dequant(a, a_s, K, fmt, dtype=torch.float32).double()
+    wv = bn.bitnet_fp4_dequant(w, w_s, K, fmt, dtype=torch.float32).double()
+    want, mag = av[-40:] @ wv.t(), av[-40:].abs() @ wv.abs().t()
+    assert bool(((y[-40:].double() - want).abs() <= want.abs() * 2.0 ** -8 + mag * (K / 16 + 16) * 2.0 ** -22).all())
