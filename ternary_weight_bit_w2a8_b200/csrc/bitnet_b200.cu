@@ -1417,15 +1417,17 @@ BITNET_API int bitnet_fp4_tensor_scale(const void *x, int dtype, int64_t rows, i
     return fp4_by_type(dtype, [&](auto dt) {
         constexpr int D = decltype(dt)::value;
         using T = typename Fp4Type<D>::T;
-        int64_t blocks = ceil_div(rows * ceil_div(K, kFp4ScalePiece<D>), kThreads / 32);
-        if (blocks > 4 * dev->sm_count) blocks = 4 * dev->sm_count;  // one wave: as many as fit
-        if (blocks < 1) blocks = 1;
-        if (blocks > 1) {
-            const int rc1 = launched(launch_pdl(fp4_clear_kernel, dim3(1), dim3(1), (size_t)0, st, g));
-            if (rc1 != BITNET_OK) return rc1;
+        const int64_t need = ceil_div(rows * ceil_div(K, kFp4ScalePiece<D>), kThreads / 32);
+        if (need <= kFp4ScaleCluster) {  // one cluster
+            const unsigned n = (unsigned)(need < 1 ? 1 : need);
+            return launched(launch_pdl_cluster(fp4_tensor_scale_kernel<D>, n, kThreads, n, 0, st, static_cast<const T *>(x),
+                                               rows, K, ldx, g));
         }
-        return launched(launch_pdl(fp4_tensor_scale_kernel<D>, dim3((unsigned)blocks), dim3(kThreads), (size_t)0, st,
-                                   static_cast<const T *>(x), rows, K, ldx, g));
+        const int64_t most = 4 * dev->sm_count;  // one wave: as many as fit
+        const int rc1 = launched(launch_pdl(fp4_clear_kernel, dim3(1), dim3(1), (size_t)0, st, g));
+        if (rc1 != BITNET_OK) return rc1;
+        return launched(launch_pdl(fp4_tensor_scale_kernel<D>, dim3((unsigned)(need < most ? need : most)), dim3(kThreads),
+                                   (size_t)0, st, static_cast<const T *>(x), rows, K, ldx, g));
     });
 }
 

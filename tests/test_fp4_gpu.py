@@ -113,7 +113,8 @@ def test_quant_non_finite_and_tiny(fmt):
 
 
 @pytest.mark.parametrize("dt", list(TYPES))
-@pytest.mark.parametrize("rows,K,pad", [(1, 1, 0), (3, 77, 1), (500, 1031, 0), (2048, 2560, 8)])
+@pytest.mark.parametrize("rows,K,pad", [(1, 1, 0), (3, 77, 1), (9, 2560, 0), (33, 2560, 1), (64, 2048, 0), (500, 1031, 0),
+                                        (2048, 2560, 8)])
 def test_tensor_scale(dt, rows, K, pad):
     t, x = activations(rows, K, TYPES[dt], K)
     t[rows // 2, K // 2] = float("inf")
