@@ -1105,10 +1105,10 @@ int fp4_pair_width(int64_t M, int64_t N, int64_t K, int format) {
     return best;
 }
 
-template <int FMT, int BT>
+template <int FMT, int BT, bool VEC>
 int launch_fp4_pair_variant(DeviceInfo *dev, const CUtensorMap &amap, const CUtensorMap &wmap, const CUtensorMap &samap,
                             const CUtensorMap &swmap, const Fp4PairArgs &a, cudaStream_t st) {
-    auto kern = fp4_pair_kernel<FMT, BT>;
+    auto kern = fp4_pair_kernel<FMT, BT, VEC>;
     constexpr size_t smem = Fp4Pair<FMT, BT>::kBytes + 1024;
     static std::atomic<uint64_t> set{0};
     if (!fp4_opt_in(dev, kern, smem, set)) return BITNET_ERR_CUDA;
@@ -1142,16 +1142,22 @@ int launch_fp4_pair(DeviceInfo *dev, const uint8_t *codes, const uint8_t *sa, co
     a.ytype = dtype;
     a.tiles_m = (int)ceil_div(M, 256);
     a.tiles_n = (int)ceil_div(N, BT);
-    a.vec = aligned(y, 16) && ldy % 8 == 0;
     a.test_stall = fp4_test_stall('3');
+    // rows of y on 16-byte boundaries have kernels of their own (one for both
+    // kept them 3 % longer)
+    const bool vec = fp4_rows_aligned(y, ldy, 2);
     return fp4_by_format(format, [&](auto fm) {
-        constexpr int F = decltype(fm)::value;
+        auto go = [&](auto bt) {
+            constexpr int F = decltype(fm)::value, B = decltype(bt)::value;
+            return vec ? launch_fp4_pair_variant<F, B, true>(dev, amap, wmap, samap, swmap, a, st)
+                       : launch_fp4_pair_variant<F, B, false>(dev, amap, wmap, samap, swmap, a, st);
+        };
         switch (BT) {
-            case 64: return launch_fp4_pair_variant<F, 64>(dev, amap, wmap, samap, swmap, a, st);
-            case 128: return launch_fp4_pair_variant<F, 128>(dev, amap, wmap, samap, swmap, a, st);
-            case 192: return launch_fp4_pair_variant<F, 192>(dev, amap, wmap, samap, swmap, a, st);
-            case 384: return launch_fp4_pair_variant<F, 384>(dev, amap, wmap, samap, swmap, a, st);
-            default: return launch_fp4_pair_variant<F, 256>(dev, amap, wmap, samap, swmap, a, st);
+            case 64: return go(std::integral_constant<int, 64>{});
+            case 128: return go(std::integral_constant<int, 128>{});
+            case 192: return go(std::integral_constant<int, 192>{});
+            case 256: return go(std::integral_constant<int, 256>{});
+            default: return go(std::integral_constant<int, 384>{});
         }
     });
 }

@@ -178,12 +178,13 @@ def test_product(fmt, M, N, K):
     g = 2.0 ** -6 / np.sqrt(K)
     ga = torch.tensor([0.75], dtype=torch.float32, device="cuda")
     gw = torch.tensor([g], dtype=torch.float32, device="cuda")
-    pad = [0, 8, 3][K % 3]
-    out = Guarded(torch, (M, N + pad), dtype, fill=7.0)
-    bn.bitnet_fp4_gemm(a, a_s, w, w_s, K, fmt, ga=ga, gw=gw, y=out.t[:, :N])
-    out.check("y")
-    assert bool((out.t[:, N:] == 7.0).all())
-    check_product(out.t[:, :N], ca, sa, cw, sw, fmt, K, 0.75 * float(gw.item()))
+    for first, pad in [(0, [0, 8, 3][K % 3]), (1, [2, 3][N % 2])]:  # and rows off every boundary
+        out = Guarded(torch, (M, first + N + pad), dtype, fill=7.0)
+        y = out.t[:, first:first + N]
+        bn.bitnet_fp4_gemm(a, a_s, w, w_s, K, fmt, ga=ga, gw=gw, y=y)
+        out.check("y")
+        assert bool((out.t[:, :first] == 7.0).all()) and bool((out.t[:, first + N:] == 7.0).all())
+        check_product(y, ca, sa, cw, sw, fmt, K, 0.75 * float(gw.item()))
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
