@@ -1090,37 +1090,51 @@ int launch_fp4_small(DeviceInfo *dev, const uint8_t *codes, int xtype, const uin
 // bring more scales.  2048 x 13824 x 2560 MX takes 62, 38, 33, 30.0 and 29.7 us
 // with 64, 128, 192, 256 and 384 rows, 512 x 6912 x 2560 11.4, 9.9, 7.7, 8.8
 // and 10.8.
-int fp4_pair_width(int64_t M, int64_t N, int64_t K, int format) {
+//   Where tiles of 64 or 128 rows leave pairs idle and k is long, 2 or 4 pairs
+// share a tile (clusters of 4 or 8 CTAs, which fill some 64 pairs' SMs at once)
+// for an exchange of some kExchange ns: 100 x 500 x 20000 MX takes 21.6 us with
+// one pair to a tile, 12.3 with two, 8.3 with four; 448 x 1664 x 18022 19.4
+// with one, 14.7 with two and 128 rows.
+struct Fp4PairPlan {
+    int width, split;
+};
+Fp4PairPlan fp4_pair_plan(int64_t M, int64_t N, int64_t K, int format) {
     constexpr int kWidths[5] = {384, 256, 192, 128, 64};
     constexpr int kStage[2][5] = {{490, 358, 288, 240, 207}, {520, 385, 345, 241, 207}};
-    constexpr int kEnd[5] = {1400, 760, 590, 410, 370};
+    constexpr int kEnd[5] = {1400, 760, 590, 410, 370}, kExchange = 200;
     const int64_t nk = ceil_div(k_pad(K), kFp4StageK), tm = ceil_div(M, 256);
-    int best = 256;
+    Fp4PairPlan best{256, 1};
     int64_t cost = INT64_MAX;
     for (int i = 0; i < 5; ++i) {
-        const int64_t rounds = ceil_div(tm * ceil_div(N, kWidths[i]), 74);
-        const int64_t c = rounds * (nk * kStage[format == BITNET_FP4_MX ? 0 : 1][i] + kEnd[i]);
-        if (c < cost) cost = c, best = kWidths[i];
+        const int64_t tiles = tm * ceil_div(N, kWidths[i]);
+        for (int s = 1; s <= (kWidths[i] <= 128 ? 4 : 1); s *= 2) {
+            if (s > 1 && (tiles * s > 64 || nk < 4 * s)) break;
+            const int64_t c = ceil_div(tiles * s, 74) * (ceil_div(nk, s) * kStage[format == BITNET_FP4_MX ? 0 : 1][i] + kEnd[i]) +
+                              (s > 1 ? kExchange : 0);
+            if (c < cost) cost = c, best = {kWidths[i], s};
+        }
     }
     return best;
 }
 
-template <int FMT, int BT, bool VEC>
+template <int FMT, int BT, bool VEC, bool SPLIT>
 int launch_fp4_pair_variant(DeviceInfo *dev, const CUtensorMap &amap, const CUtensorMap &wmap, const CUtensorMap &samap,
                             const CUtensorMap &swmap, const Fp4PairArgs &a, cudaStream_t st) {
-    auto kern = fp4_pair_kernel<FMT, BT, VEC>;
+    auto kern = fp4_pair_kernel<FMT, BT, VEC, SPLIT>;
     constexpr size_t smem = Fp4Pair<FMT, BT>::kBytes + 1024;
     static std::atomic<uint64_t> set{0};
     if (!fp4_opt_in(dev, kern, smem, set)) return BITNET_ERR_CUDA;
     const int64_t units = (int64_t)a.tiles_m * a.tiles_n, pairs = dev->sm_count / 2;
-    return launched(launch_pdl_cluster(kern, (unsigned)(2 * (units < pairs ? units : pairs)), kFp4PairThreads, 0, smem, st,
-                                       amap, wmap, samap, swmap, a));
+    const int64_t used = SPLIT ? units * a.split : (units < pairs ? units : pairs);
+    return launched(launch_pdl_cluster(kern, (unsigned)(2 * used), kFp4PairThreads, (unsigned)(SPLIT ? 2 * a.split : 2),
+                                       smem, st, amap, wmap, samap, swmap, a));
 }
 
 int launch_fp4_pair(DeviceInfo *dev, const uint8_t *codes, const uint8_t *sa, const float *ga, const uint8_t *w,
                     const uint8_t *sw, const float *gw, int format, void *y, int dtype, int64_t M, int64_t N, int64_t K,
                     int64_t ldy, cudaStream_t st) {
-    const int BT = fp4_pair_width(M, N, K, format);
+    const Fp4PairPlan plan = fp4_pair_plan(M, N, K, format);
+    const int BT = plan.width;
     if (ceil_div(M, 256) * ceil_div(N, BT) > (int64_t)1 << 30) return BITNET_ERR_UNSUPPORTED;
     const int64_t tiles = fp4_scale_tiles(K, format);
     if ((ceil_div(M, 128) + 1) * tiles > INT32_MAX || (ceil_div(N, 128) + 3) * tiles > INT32_MAX ||
@@ -1142,6 +1156,7 @@ int launch_fp4_pair(DeviceInfo *dev, const uint8_t *codes, const uint8_t *sa, co
     a.ytype = dtype;
     a.tiles_m = (int)ceil_div(M, 256);
     a.tiles_n = (int)ceil_div(N, BT);
+    a.split = plan.split;
     a.test_stall = fp4_test_stall('3');
     // rows of y on 16-byte boundaries have kernels of their own (one for both
     // kept them 3 % longer)
@@ -1149,8 +1164,10 @@ int launch_fp4_pair(DeviceInfo *dev, const uint8_t *codes, const uint8_t *sa, co
     return fp4_by_format(format, [&](auto fm) {
         auto go = [&](auto bt) {
             constexpr int F = decltype(fm)::value, B = decltype(bt)::value;
-            return vec ? launch_fp4_pair_variant<F, B, true>(dev, amap, wmap, samap, swmap, a, st)
-                       : launch_fp4_pair_variant<F, B, false>(dev, amap, wmap, samap, swmap, a, st);
+            if constexpr (B <= 128)
+                if (plan.split > 1) return launch_fp4_pair_variant<F, B, false, true>(dev, amap, wmap, samap, swmap, a, st);
+            return vec ? launch_fp4_pair_variant<F, B, true, false>(dev, amap, wmap, samap, swmap, a, st)
+                       : launch_fp4_pair_variant<F, B, false, false>(dev, amap, wmap, samap, swmap, a, st);
         };
         switch (BT) {
             case 64: return go(std::integral_constant<int, 64>{});

@@ -32,6 +32,7 @@ struct Fp4PairArgs {
     void *y;
     int ytype;
     int tiles_m, tiles_n;  // 256-token and BT-row tiles
+    int split;             // SPLIT: pairs to a tile, in one cluster
     int test_stall;        // the first pair never asks for its first stage (test of the bounded waits)
 };
 
@@ -65,6 +66,7 @@ struct Fp4Pair {
     static_assert(kHalves == 1 || BT % 128 == 0, "whole bands");
     static_assert(kStage % 1024 == 0 && kCols / 2 * 128 % 1024 == 0, "swizzled rows");
     static_assert(kBytes + 1024 <= 232448, "shared memory");
+    static_assert(BT > 128 || 128 * (BT * 4 + 16) <= kOutAt, "sums of a split tile take the stages' place");
 };
 
 // A TMA load of one CTA of a pair that completes on a barrier of either (an
@@ -102,13 +104,13 @@ __device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t des
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-// Arrives on the barrier at this offset in both CTAs once the tensor-core work
-// issued so far is done.
-__device__ __forceinline__ void umma_commit_pair(uint64_t *bar) {
+// Arrives on the barrier at this offset in both CTAs (`lead` is the cluster rank
+// of the first) once the tensor-core work issued so far is done.
+__device__ __forceinline__ void umma_commit_pair(uint64_t *bar, uint32_t lead) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_u32(bar)),
-        "h"((uint16_t)3)
+        "h"((uint16_t)(3u << lead))
         : "memory");
 }
 
@@ -245,8 +247,12 @@ __device__ __forceinline__ void store_box(const Fp4PairArgs &a, uint8_t *box, co
     }
 }
 
-template <int FMT, int BT, bool VEC>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
+// VEC: rows of y start on 16-byte boundaries.  SPLIT: for few tiles over a long
+// k, a.split pairs share a tile (a cluster, and no tile after it): each sums a
+// range of k, puts its sums into its stages' place and, once all have, adds up
+// and stores its share of the rows, in the pairs' order.
+template <int FMT, int BT, bool VEC, bool SPLIT>
+__global__ void __launch_bounds__(kFp4PairThreads, 1)
     fp4_pair_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
                     const __grid_constant__ CUtensorMap samap, const __grid_constant__ CUtensorMap swmap,
                     const Fp4PairArgs a) {
@@ -262,11 +268,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
+    const uint32_t lead = cluster_rank() & ~1u, rank = cluster_rank() & 1u;  // the pair's first CTA, and which this is
     const int units = a.tiles_m * a.tiles_n;
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int pair = SPLIT ? (int)blockIdx.x / (2 * a.split) : blockIdx.x >> 1, pairs = SPLIT ? units : gridDim.x >> 1;
     const int64_t kp = k_pad(a.K);
-    const int nk = (int)ceil_div(kp, kFp4StageK);
+    const int stages = (int)ceil_div(kp, kFp4StageK);
+    const int part_k = (int)lead >> 1;  // SPLIT: the pair in its cluster
+    const int k0 = SPLIT ? (int)((int64_t)stages * part_k / a.split) : 0;
+    const int nk = SPLIT ? (int)((int64_t)stages * (part_k + 1) / a.split) : stages;  // this pair's stages: k0 .. nk - 1
     const int tiles = (int)fp4_scale_tiles(a.K, FMT);
 
     if (threadIdx.x == 0) {
@@ -308,7 +317,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
             const int tm = u % a.tiles_m, tn = u / a.tiles_m;
             const int m0 = tm * 256 + (int)rank * 128;
             const int64_t n0 = (int64_t)tn * BT;
-            for (int i = 0; i < nk; ++i, ++g) {
+            for (int i = k0; i < nk; ++i, ++g) {
                 const int s = g % S;
                 if (g >= S && !warp_wait(&empty[s], (uint32_t)(g / S - 1) & 1u, abort_flag)) {
                     ok = false;
@@ -317,7 +326,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
                 if (a.test_stall && pair == 0 && g == 0) continue;
                 if (elect_one()) {
                     uint8_t *st = sm + s * L::kStage;
-                    const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
+                    const uint32_t bar = map_rank(smem_u32(&full[s]), lead);
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * L::kStage);
                     tma_load_pair(st, &amap, i * 128, m0, bar);
 #pragma unroll
@@ -360,7 +369,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
                 const uint32_t off = BT % 128 == 0 ? 0 : 2 * ((uint32_t)(u / a.tiles_m) & 1);
                 const int d = L::kHalves == 2 ? 0 : li & 1;
                 if (L::kHalves == 1 && !(ok = acc_free(d, li >> 1))) break;
-                for (int i = 0; i < nk; ++i, ++g) {
+                for (int i = k0; i < nk; ++i, ++g) {
                     if (!tc_wait(&full[s], phase, abort_flag) ||
                         (L::kSlots < S && g >= L::kSlots &&
                          !tc_wait(&empty[(g - L::kSlots) % S], (uint32_t)((g - L::kSlots) / S) & 1u, abort_flag))) {
@@ -371,7 +380,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
                     const uint64_t at = (uint64_t)(s * (L::kStage >> 4));
                     const uint32_t ca = tmem + (uint32_t)(2 * L::kCols + slot * L::kSlotCols), cw = ca + 4 * L::kTiles;
                     const bool whole = i < full_stages;
-                    const uint32_t more = i > 0 ? 1u : 0u;
+                    const uint32_t more = i > k0 ? 1u : 0u;
 #pragma unroll
                     for (int t = 0; t < L::kTiles; ++t) {
                         if (t < L::kTiles / 2 || whole) {
@@ -394,23 +403,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
                                                    cw + 4 * t * L::kBands + off + h * (L::kCols / 32), j > 0 ? 1u : more);
                         }
                     };
-                    if (L::kHalves == 2 && i == 0 && !(ok = acc_free(0, li))) break;
+                    if (L::kHalves == 2 && i == k0 && !(ok = acc_free(0, li))) break;
                     multiply(0);
                     if constexpr (L::kHalves == 2) {
-                        if (i + 1 == nk) umma_commit_pair(&acc_full[0]);
-                        if (i == 0 && !(ok = acc_free(1, li))) break;
+                        if (i + 1 == nk) umma_commit_pair(&acc_full[0], lead);
+                        if (i == k0 && !(ok = acc_free(1, li))) break;
                         multiply(1);
                     }
-                    umma_commit_pair(&empty[s]);
+                    umma_commit_pair(&empty[s], lead);
                     if (++s == S) s = 0, phase ^= 1;
                     if (++slot == L::kSlots) slot = 0;
                 }
                 if (!ok) break;
-                umma_commit_pair(&acc_full[L::kHalves == 2 ? 1 : d]);
+                umma_commit_pair(&acc_full[L::kHalves == 2 ? 1 : d], lead);
             }
             if (!ok) {
                 // the MMAs issued so far end before tensor memory is freed
-                umma_commit_pair(drain);
+                umma_commit_pair(drain, lead);
                 mbar_wait_bounded(drain, 0);
             }
         }
@@ -425,6 +434,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
         const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(part * kMost * 32);
         uint8_t *box = sm + L::kOutAt + (warp - 2) * 4096;
         const float gs = (a.ga != nullptr ? *a.ga : 1.0f) * (a.gw != nullptr ? *a.gw : 1.0f);
+        if constexpr (SPLIT) {
+            // this pair's sums as they are: rows of BT floats and 16 bytes more, so that the lanes' rows share no banks
+            if (warp_wait(&acc_full[0], 0u, abort_flag)) {
+                tc_fence_after();
+                uint8_t *row = sm + (quarter * 32 + lane) * (BT * 4 + 16) + part * kMost * 128;
+#pragma unroll
+                for (int c = 0; c < kMost; ++c) {
+                    if (c >= groups) break;
+                    uint32_t f[32];
+                    tmem_ld32(t0 + (uint32_t)(32 * c), f);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4 *>(row + c * 128 + 16 * i) =
+                            make_uint4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                }
+            }
+        }
         // waits for use `use` of accumulator d, reads this warp's part of it as 16-bit pairs and releases it
         auto empty_acc = [&](int d, int use, uint32_t (&v)[16 * kMost]) -> bool {
             if (!warp_wait(&acc_full[d], (uint32_t)use & 1u, abort_flag)) return false;
@@ -436,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&acc_empty[d]), 0));
+            if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&acc_empty[d]), lead));
             if (a.ytype == BITNET_FP16)
                 pack_all<BITNET_FP16, 16 * kMost>(v, f, gs);
             else
@@ -454,7 +481,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
             }
         };
         int li = 0;
-        for (int u = pair; u < units; u += pairs, ++li) {
+        for (int u = pair; !SPLIT && u < units; u += pairs, ++li) {
             const int64_t m0 = (int64_t)(u % a.tiles_m) * 256 + rank * 128 + quarter * 32;
             const int64_t n0 = (int64_t)(u / a.tiles_m) * BT + part * kMost * 32;
             uint32_t v[16 * kMost];
@@ -472,6 +499,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp4PairThreads, 1)
         __syncwarp();
     }
     tc_fence_before();
+    if constexpr (SPLIT) {
+        cluster_sync();  // every pair's sums are in its shared memory
+        const float gs = (a.ga != nullptr ? *a.ga : 1.0f) * (a.gw != nullptr ? *a.gw : 1.0f);
+        const int rows = 128 / a.split, r0 = part_k * rows;
+        const int64_t m0 = (int64_t)(pair % a.tiles_m) * 256 + rank * 128, n0 = (int64_t)(pair / a.tiles_m) * BT;
+        const bool words = ((reinterpret_cast<uintptr_t>(a.y) | (uintptr_t)(2 * a.ldy)) & 7) == 0;
+        for (int e = threadIdx.x; e < rows * (BT / 4); e += kFp4PairThreads) {
+            const int row = r0 + e / (BT / 4), c = 4 * (e % (BT / 4));
+            const int64_t m = m0 + row, n = n0 + c;
+            if (m >= a.M || n >= a.N) continue;
+            const uint32_t at = smem_u32(sm) + (uint32_t)(row * (BT * 4 + 16) + c * 4);
+            float4 t = ld_cluster_v4(map_rank(at, rank));
+            for (int q = 1; q < a.split; ++q) {
+                const float4 o = ld_cluster_v4(map_rank(at, 2 * q + rank));
+                t.x += o.x, t.y += o.y, t.z += o.z, t.w += o.w;
+            }
+            const float v[4] = {__fmul_rn(t.x, gs), __fmul_rn(t.y, gs), __fmul_rn(t.z, gs), __fmul_rn(t.w, gs)};
+            if (words && n + 4 <= a.N) {
+                const uint2 p = a.ytype == BITNET_FP16
+                                    ? make_uint2(pack2<BITNET_FP16>(v[0], v[1]), pack2<BITNET_FP16>(v[2], v[3]))
+                                    : make_uint2(pack2<BITNET_BF16>(v[0], v[1]), pack2<BITNET_BF16>(v[2], v[3]));
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.y) + m * a.ldy + n) = p;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (n + i < a.N) fp4_store(a.y, m * a.ldy + n + i, v[i], a.ytype);
+            }
+        }
+    }
     __syncthreads();
     cluster_sync_relaxed();  // neither CTA signals the other or reads its shared memory any more
     if (warp == 1) {

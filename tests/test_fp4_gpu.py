@@ -163,7 +163,8 @@ SHAPES = [(1, 1, 1), (1, 128, 128), (1, 2560, 2560), (2, 129, 64), (3, 300, 1000
           (17, 640, 512), (31, 96, 4100), (64, 513, 2560), (65, 100, 130), (100, 777, 1024), (128, 1000, 260),
           (129, 333, 700), (200, 1000, 2560), (257, 129, 5120), (513, 1100, 384), (1000, 640, 65), (1, 5, 20000),
           (600, 600, 600), (300, 20000, 256), (2100, 5000, 512), (520, 9700, 1000), (1030, 11111, 192),
-          (510, 7001, 3000), (2048, 2560, 2000), (700, 4700, 256)]
+          (510, 7001, 3000), (2048, 2560, 2000), (700, 4700, 256),
+          (130, 300, 5000), (70, 1501, 4801), (300, 700, 4100), (448, 800, 9000), (65, 200, 16000)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)

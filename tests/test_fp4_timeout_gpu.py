@@ -43,9 +43,9 @@ print(json.dumps({"status": status, "again": again, "right_after": right, "secon
 """
 
 
-# one CTA per tile; a cluster; tokens quantised in the launch; the pair kernel
+# one CTA per tile; a cluster; tokens quantised in the launch; the pair kernel, four pairs to a tile and one
 @pytest.mark.parametrize("stall,args", [("2", (20, 300, 700, 0)), ("2", (1, 600, 6912, 0)), ("2", (3, 600, 6912, 1)),
-                                        ("3", (200, 1000, 5120, 0))])
+                                        ("3", (200, 200, 5120, 0)), ("3", (300, 9000, 512, 0))])
 def test_bounded_wait_reports_timeout_and_context_survives(stall, args):
     torch = pytest.importorskip("torch")
     if not torch.cuda.is_available():
