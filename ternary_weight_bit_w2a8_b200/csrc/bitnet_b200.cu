@@ -1087,7 +1087,10 @@ int launch_fp4_small(DeviceInfo *dev, const uint8_t *codes, int xtype, const uin
 // B200's 74 pairs take the least time.  Measured on 2048 x 9472 x K: a 256-k
 // stage of a tile takes kStage ns and the tile kEnd more (its accumulators are
 // emptied while the next tile's first MMAs wait, or run beside).  NV stages
-// bring more scales.  2048 x 13824 x 2560 MX takes 62, 38, 33, 30.0 and 29.7 us
+// bring more scales.  A tile's stores run beside the next tile and take kLeast
+// ns, which a short k does not cover, and more where rows of y are off 16-byte
+// boundaries (1791 x 6643 x 1113: 22.5, 17.5, 20.0, 15.9 and 22.3 us with 384
+// to 64 rows).  2048 x 13824 x 2560 MX takes 62, 38, 33, 30.0 and 29.7 us
 // with 64, 128, 192, 256 and 384 rows, 512 x 6912 x 2560 11.4, 9.9, 7.7, 8.8
 // and 10.8.
 //   Where tiles of 64 or 128 rows leave pairs idle and k is long, 2 or 4 pairs
@@ -1098,23 +1101,30 @@ int launch_fp4_small(DeviceInfo *dev, const uint8_t *codes, int xtype, const uin
 struct Fp4PairPlan {
     int width, split;
 };
-Fp4PairPlan fp4_pair_plan(int64_t M, int64_t N, int64_t K, int format) {
+Fp4PairPlan fp4_pair_plan(int64_t M, int64_t N, int64_t K, int format, bool vec) {
     constexpr int kWidths[5] = {384, 256, 192, 128, 64};
     constexpr int kStage[2][5] = {{490, 358, 288, 240, 207}, {520, 385, 345, 241, 207}};
     constexpr int kEnd[5] = {1400, 760, 590, 410, 370}, kExchange = 200;
+    constexpr int kLeast[2][5] = {{2900, 1410, 1300, 760, 710}, {9000, 4500, 3900, 2300, 1800}};
     const int64_t nk = ceil_div(k_pad(K), kFp4StageK), tm = ceil_div(M, 256);
-    Fp4PairPlan best{256, 1};
-    int64_t cost = INT64_MAX;
-    for (int i = 0; i < 5; ++i) {
-        const int64_t tiles = tm * ceil_div(N, kWidths[i]);
-        for (int s = 1; s <= (kWidths[i] <= 128 ? 4 : 1); s *= 2) {
-            if (s > 1 && (tiles * s > 64 || nk < 4 * s)) break;
-            const int64_t c = ceil_div(tiles * s, 74) * (ceil_div(nk, s) * kStage[format == BITNET_FP4_MX ? 0 : 1][i] + kEnd[i]) +
-                              (s > 1 ? kExchange : 0);
-            if (c < cost) cost = c, best = {kWidths[i], s};
+    auto plan = [&](int most, int off) {
+        Fp4PairPlan best{256, 1};
+        int64_t cost = INT64_MAX;
+        for (int i = 0; i < 5; ++i) {
+            const int64_t tiles = tm * ceil_div(N, kWidths[i]);
+            for (int s = 1; s <= (kWidths[i] <= 128 ? most : 1); s *= 2) {
+                if (s > 1 && (tiles * s > 64 || nk < 4 * s)) break;
+                const int64_t t = ceil_div(nk, s) * kStage[format == BITNET_FP4_MX ? 0 : 1][i] + kEnd[i];
+                const int64_t c = ceil_div(tiles * s, 74) * (t > kLeast[off][i] ? t : kLeast[off][i]) + (s > 1 ? kExchange : 0);
+                if (c < cost) cost = c, best = {kWidths[i], s};
+            }
         }
-    }
-    return best;
+        return best;
+    };
+    // the split, which groups the sums, follows from the sizes alone; the width
+    // leaves each sum's order as it is and may follow y's alignment too
+    const Fp4PairPlan best = plan(4, 0);
+    return vec || best.split > 1 ? best : plan(1, 1);
 }
 
 template <int FMT, int BT, bool VEC, bool SPLIT>
@@ -1133,7 +1143,10 @@ int launch_fp4_pair_variant(DeviceInfo *dev, const CUtensorMap &amap, const CUte
 int launch_fp4_pair(DeviceInfo *dev, const uint8_t *codes, const uint8_t *sa, const float *ga, const uint8_t *w,
                     const uint8_t *sw, const float *gw, int format, void *y, int dtype, int64_t M, int64_t N, int64_t K,
                     int64_t ldy, cudaStream_t st) {
-    const Fp4PairPlan plan = fp4_pair_plan(M, N, K, format);
+    // rows of y on 16-byte boundaries have kernels of their own (one for both
+    // kept them 3 % longer)
+    const bool vec = fp4_rows_aligned(y, ldy, 2);
+    const Fp4PairPlan plan = fp4_pair_plan(M, N, K, format, vec);
     const int BT = plan.width;
     if (ceil_div(M, 256) * ceil_div(N, BT) > (int64_t)1 << 30) return BITNET_ERR_UNSUPPORTED;
     const int64_t tiles = fp4_scale_tiles(K, format);
@@ -1158,9 +1171,6 @@ int launch_fp4_pair(DeviceInfo *dev, const uint8_t *codes, const uint8_t *sa, co
     a.tiles_n = (int)ceil_div(N, BT);
     a.split = plan.split;
     a.test_stall = fp4_test_stall('3');
-    // rows of y on 16-byte boundaries have kernels of their own (one for both
-    // kept them 3 % longer)
-    const bool vec = fp4_rows_aligned(y, ldy, 2);
     return fp4_by_format(format, [&](auto fm) {
         auto go = [&](auto bt) {
             constexpr int F = decltype(fm)::value, B = decltype(bt)::value;

@@ -19,6 +19,8 @@
 // that the first half's MMAs run while the second half is emptied).
 #pragma once
 
+#include <type_traits>
+
 #include "fp4_gemm.cuh"
 
 namespace bitnet {
@@ -160,8 +162,8 @@ __device__ __forceinline__ void pack_all(uint32_t (&v)[N], const uint32_t *f, fl
 //   Rows of y off 16-byte boundaries are stored as the 4-byte words that lie on
 // 4-byte boundaries of y: a lane whose row starts between two puts its pairs
 // down shifted by one value, and stores the row's first and last value itself.
-// (2047 x 13823 x 2560 MX takes 45 us; 55 where each lane puts its words
-// together from two reads, 63 where those were not batched.)
+// (2047 x 13823 x 2560 MX takes 40 us; 55 where each lane puts its words
+// together from two reads.)
 template <bool VEC, int N>
 __device__ __forceinline__ void store_box(const Fp4PairArgs &a, uint8_t *box, const uint32_t (&v)[N], int at, int pieces,
                                           uint16_t *y, int rows, int64_t nb, int lane) {
@@ -202,14 +204,21 @@ __device__ __forceinline__ void store_box(const Fp4PairArgs &a, uint8_t *box, co
     if constexpr (VEC) {
         const int w = lane & (pieces - 1), step = 32 / pieces;
         const int64_t n = nb + 8 * w;
-        if (pieces == 8 && rows == 32 && cols == 64) {  // a whole box: every row is read before the first is stored
-            uint4 t[8];
-            const int r0 = lane >> 3;
+        if (rows == 32 && cols == width) {  // a whole box: every row is read before the first is stored
+            auto whole = [&](auto p) {
+                constexpr int kPieces = decltype(p)::value, kStep = 32 / kPieces;
+                uint4 t[kPieces];
+                const int r0 = lane / kPieces;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                t[i] = *reinterpret_cast<const uint4 *>(box + (r0 + 4 * i) * 128 + ((w ^ ((r0 + 4 * i) & 7)) << 4));
+                for (int i = 0; i < kPieces; ++i)
+                    t[i] = *reinterpret_cast<const uint4 *>(box + (r0 + kStep * i) * 128 + ((w ^ ((r0 + kStep * i) & 7)) << 4));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(y + (r0 + 4 * i) * a.ldy + n) = t[i];
+                for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint4 *>(y + (r0 + kStep * i) * a.ldy + n) = t[i];
+            };
+            if (pieces == 8)
+                whole(std::integral_constant<int, 8>{});
+            else
+                whole(std::integral_constant<int, 4>{});
             return;
         }
         for (int r = lane / pieces; r < rows; r += step) {
@@ -226,7 +235,26 @@ __device__ __forceinline__ void store_box(const Fp4PairArgs &a, uint8_t *box, co
         }
     } else {
         if (lane >= width / 2) return;
-        // eight rows are read before the first is stored (one by one, a store holds up the next row's read)
+        if (rows == 32 && cols == width) {  // a whole box: even and odd rows each have their shift, pointer and lanes
+            const int odd0 = first_odd, odd1 = (first_odd + step_odd) & 1;
+            const bool go0 = lane > 0 || !odd0, go1 = lane > 0 || !odd1;
+            uint16_t *y0 = y + nb + 2 * lane - odd0, *y1 = y + nb + 2 * lane - odd1 + a.ldy;
+            const int64_t step = 2 * a.ldy;
+            const uint8_t *from = box + 4 * (lane & 3);
+#pragma unroll
+            for (int r0 = 0; r0 < 32; r0 += 8) {  // eight rows are read before the first is stored
+                uint32_t t[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    t[i] = *reinterpret_cast<const uint32_t *>(from + (r0 + i) * 128 + (((lane >> 2) ^ i) << 4));
+#pragma unroll
+                for (int i = 0; i < 8; i += 2, y0 += step, y1 += step) {
+                    if (go0) *reinterpret_cast<uint32_t *>(y0) = t[i];
+                    if (go1) *reinterpret_cast<uint32_t *>(y1) = t[i + 1];
+                }
+            }
+            return;
+        }
         const uint8_t *br = box + 4 * (lane & 3);
         uint16_t *yr = y + nb + 2 * lane;
         for (int r0 = 0; r0 < rows; r0 += 8, br += 1024, yr += 8 * a.ldy) {
