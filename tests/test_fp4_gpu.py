@@ -189,6 +189,20 @@ def test_product(fmt, M, N, K):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(3, 300, 1000), (65, 200, 16000), (130, 300, 5000), (513, 6643, 1113), (2047, 5000, 300)])
+def test_product_bits_do_not_depend_on_rows_of_y(fmt, M, N, K):
+    """The same sums whatever boundaries the rows of y start on."""
+    rng = np.random.default_rng(K)
+    a, a_s = device_matrix(*ref.random_matrix(M, K, fmt, rng), fmt)
+    w, w_s = device_matrix(*ref.random_matrix(N, K, fmt, rng), fmt)
+    ldy = -(-N // 8) * 8 + 8
+    want = bn.bitnet_fp4_gemm(a, a_s, w, w_s, K, fmt, y=torch.empty(M, ldy, dtype=torch.float16, device="cuda")[:, :N])
+    for first, pad in [(1, 0), (2, 0), (4, 1)]:
+        y = torch.empty(M, ldy + pad, dtype=torch.float16, device="cuda")[:, first:first + N]
+        assert torch.equal(bn.bitnet_fp4_gemm(a, a_s, w, w_s, K, fmt, y=y), want)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("M", [1, 40, 300])
 def test_product_of_nan_scales(fmt, M):
     """A NaN block makes its row NaN and no other."""
