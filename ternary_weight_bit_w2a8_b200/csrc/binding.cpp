@@ -79,7 +79,7 @@ int64_t row_stride(const at::Tensor &t, const char *name) {
 float *scalar(PyObject *o, c10::Device d, const char *name) {
     if (o == Py_None) return nullptr;
     const at::Tensor &t = tensor(o, name);
-    if (t.scalar_type() != at::kFloat || t.device() != d || t.numel() < 1)
+    if (t.scalar_type() != at::kFloat || t.device() != d || t.numel() != 1)
         refuse(std::string(name) + " must be a float32 tensor of one value on the call's CUDA device, not " + shown(t));
     return static_cast<float *>(t.data_ptr());
 }
