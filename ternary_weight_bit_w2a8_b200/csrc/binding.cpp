@@ -111,20 +111,22 @@ at::Tensor fresh(at::IntArrayRef size, at::ScalarType type, c10::Device d) {
     return at::detail::empty_cuda(size, type, d, std::nullopt);
 }
 
-// y as given, or a new [rows, cols] of the type asked for (bfloat16 if none).
+// y as given (of the type asked for, if one is), or a new [rows, cols] of that type (bfloat16 if none).
 at::Tensor output(PyObject *oy, PyObject *odtype, int64_t rows, int64_t cols, c10::Device d, int64_t *ld) {
+    at::ScalarType type = at::kBFloat16;
+    if (odtype != Py_None) {
+        if (!THPDtype_Check(odtype)) refuse("dtype must be a torch.dtype");
+        type = reinterpret_cast<THPDtype *>(odtype)->scalar_type;
+    }
     if (oy == Py_None) {
-        at::ScalarType type = at::kBFloat16;
-        if (odtype != Py_None) {
-            if (!THPDtype_Check(odtype)) refuse("dtype must be a torch.dtype");
-            type = reinterpret_cast<THPDtype *>(odtype)->scalar_type;
-        }
         float_type(type, "dtype");
         *ld = cols;
         return fresh({rows, cols}, type, d);
     }
     at::Tensor y = tensor(oy, "y");
     on_device(y, d, "y");
+    if (odtype != Py_None && y.scalar_type() != type)
+        refuse(std::string("dtype is ") + c10::toString(type) + ", y is " + shown(y));
     *ld = row_stride(y, "y");
     if (y.size(0) != rows || y.size(1) != cols)
         refuse("y must be [" + std::to_string(rows) + ", " + std::to_string(cols) + "], not " + shown(y));

@@ -46,3 +46,22 @@ def test_one_value_of_any_shape_is_a_scale(operands, call):
     many = torch.ones(3, device="cuda")
     for g in (torch.ones((), device="cuda"), torch.ones(1, 1, device="cuda"), many[1:2]):
         SCALED[call](operands, g)
+
+
+# each call with an output and a type asked for
+TYPED = {
+    "dequant": lambda o, y, t: bn.bitnet_fp4_dequant(o[1], o[2], 256, NV, y=y, dtype=t),
+    "gemm": lambda o, y, t: bn.bitnet_fp4_gemm(*o[1:], 256, NV, y=y, dtype=t),
+    "linear": lambda o, y, t: bn.bitnet_fp4_linear(o[0], o[3], o[4], NV, y=y, dtype=t),
+}
+
+
+@pytest.mark.parametrize("call", list(TYPED))
+def test_the_type_asked_for_is_that_of_y(operands, call):
+    cols = 256 if call == "dequant" else 8
+    y = torch.empty(4, cols, dtype=torch.float16, device="cuda")
+    assert TYPED[call](operands, y, torch.float16).data_ptr() == y.data_ptr()
+    assert TYPED[call](operands, y, None).data_ptr() == y.data_ptr()
+    for t in (torch.bfloat16, torch.float32, torch.int8, "float16"):
+        with pytest.raises(ValueError, match="dtype"):
+            TYPED[call](operands, y, t)
