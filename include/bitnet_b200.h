@@ -272,7 +272,8 @@ BITNET_API int bitnet_fp4_dequant(const uint8_t *codes, const uint8_t *scales, i
  * Product of two quantised matrices of the same format:
  *   y[m, n] = round(ga * gw * sum_k A[m, k] * W[n, k]),
  * A and W the values without their tensor scales, summed in fp32 (the order
- * and the grouping of the sums depend on the sizes and the format only).
+ * and the grouping of the sums depend on the sizes and the format only); ga * gw
+ * may lie beyond fp32's range where the result does not.
  *   a, a_scales  A [M, K];  w, w_scales  W [N, K];  all 16-byte aligned
  *   ga, gw       device, 1 float each, or NULL
  *   y            device, dtype BITNET_BF16 or BITNET_FP16 [M, N], row stride

@@ -94,6 +94,20 @@ __device__ __forceinline__ void fp4_store(void *y, int64_t i, float v, int dtype
         static_cast<__nv_bfloat16 *>(y)[i] = __float2bfloat16_rn(v);
 }
 
+// ga * gw in two factors, by which a sum is multiplied one after the other:
+// their product and 1, or, where fp32 does not hold that as a normal number
+// (tensors of values around 1e-20 have such scales, and sums of 1e8 beside
+// them), 2^126 times the product and 2^-126, or 2^-126 times it and 2^126.  The
+// power goes to the smaller scale first, exactly: below 2^-63 in the one case,
+// above 1 in the other.
+__device__ __forceinline__ float2 fp4_factors(const float *ga, const float *gw) {
+    const float a = ga != nullptr ? *ga : 1.0f, b = gw != nullptr ? *gw : 1.0f, p = fabsf(__fmul_rn(a, b));
+    const bool below = p < 0x1p-126f, above = p == __uint_as_float(0x7f800000u), swap = fabsf(a) > fabsf(b);
+    const float up = below ? 0x1p126f : (above ? 0x1p-126f : 1.0f), down = below ? 0x1p-126f : (above ? 0x1p126f : 1.0f);
+    return make_float2(__fmul_rn(__fmul_rn(swap ? b : a, up), swap ? a : b), down);
+}
+__device__ __forceinline__ float fp4_scaled(float sum, float2 g) { return __fmul_rn(__fmul_rn(sum, g.x), g.y); }
+
 // ------------------------------------------------------------------ few tokens
 // Up to 64 tokens: reading the weights bounds the call.  The weights are the
 // MMA's row operand (128 rows of them a tile), the tokens its BT columns, so
@@ -388,9 +402,9 @@ __global__ void __launch_bounds__(kFp4Threads, Fp4Small<FMT, BT>::kCtas)
         const int quarter = warp & 3;
         const uint32_t t0 = tmem + ((uint32_t)(quarter * 32) << 16);
         const int row = quarter * 32 + lane;
+        const float2 g = fp4_factors(a.ga, a.gw);
         if (warp_wait(done, 0u, abort_flag)) {
             tc_fence_after();
-            const float g = (a.ga != nullptr ? *a.ga : 1.0f) * (a.gw != nullptr ? *a.gw : 1.0f);
             const int64_t n = (int64_t)tile * kFp4Rows + row;
             float *part = reinterpret_cast<float *>(sm);
 #pragma unroll 1
@@ -403,7 +417,7 @@ __global__ void __launch_bounds__(kFp4Threads, Fp4Small<FMT, BT>::kCtas)
                     if (a.split > 1)
                         part[(c + i) * kFp4Rows + row] = __uint_as_float(v[i]);
                     else if (n < a.N)
-                        fp4_store(a.y, (c + i) * a.ldy + n, __fmul_rn(__uint_as_float(v[i]), g), a.ytype);
+                        fp4_store(a.y, (c + i) * a.ldy + n, fp4_scaled(__uint_as_float(v[i]), g), a.ytype);
                 }
             }
         }
@@ -412,7 +426,7 @@ __global__ void __launch_bounds__(kFp4Threads, Fp4Small<FMT, BT>::kCtas)
     tc_fence_before();
     if (a.split > 1) {
         cluster_sync();  // every CTA's sums are in its shared memory
-        const float g = (a.ga != nullptr ? *a.ga : 1.0f) * (a.gw != nullptr ? *a.gw : 1.0f);
+        const float2 g = fp4_factors(a.ga, a.gw);
         // four neighbouring rows of a token at a time: one 16-byte read of each CTA's sums
         const int quads = kFp4Rows / 4 / a.split, r0 = rank * (kFp4Rows / a.split);
         const uint32_t base = smem_u32(sm);
@@ -429,7 +443,7 @@ __global__ void __launch_bounds__(kFp4Threads, Fp4Small<FMT, BT>::kCtas)
             const float o[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (n + i < a.N) fp4_store(a.y, c * a.ldy + n + i, __fmul_rn(o[i], g), a.ytype);
+                if (n + i < a.N) fp4_store(a.y, c * a.ldy + n + i, fp4_scaled(o[i], g), a.ytype);
         }
         cluster_sync_relaxed();  // nobody reads this CTA's shared memory any more
     } else {
