@@ -389,6 +389,7 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
         // sees both CTAs' copies; they leave together)
         if (rank == 0)
             for (int j = g - S < 0 ? 0 : g - S; j < g; ++j) mbar_wait_bounded(&full[j % S], (uint32_t)(j / S) & 1u);
+        if (!SPLIT && ok) wait_last_empty<S>(empty, g, lane, abort_flag);
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
         // One thread; what it does per stage has to stay below the MMAs' 2 BT cycles.
@@ -570,6 +571,7 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
                     if (n + i < a.N) fp4_store(a.y, m * a.ldy + n + i, v[i], a.ytype);
             }
         }
+        if (warp == 1 && !*abort_flag) wait_last_empty<S>(empty, nk - k0, lane, abort_flag);
     }
     __syncthreads();
     cluster_sync_relaxed();  // neither CTA signals the other or reads its shared memory any more
