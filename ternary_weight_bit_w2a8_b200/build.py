@@ -4,7 +4,7 @@ The CUDA runtime is linked statically and the driver API is reached through
 cudaGetDriverEntryPoint, so the library loads on a machine without a GPU
 driver (where every compute call then returns BITNET_ERR_CUDA).  Beside it the
 native binding of the 4-bit functions (_binding.so, g++ against the installed
-torch).
+torch; left out where there is none).
 """
 from __future__ import annotations
 
@@ -49,10 +49,15 @@ def up_to_date() -> bool:
     return newer(LIB, sources())
 
 
-def build_binding(force: bool = False, verbose: bool = False) -> str:
+def build_binding(force: bool = False, verbose: bool = False):
+    """Builds the binding; without torch there is nothing to bind to, and the C library is complete by itself."""
     if not force and newer(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "bitnet_b200.h")]):
         return BINDING
-    import torch
+    try:
+        import torch
+    except ImportError:
+        print("torch is not installed: the native binding of the 4-bit functions is not built", file=sys.stderr)
+        return None
     tdir = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"))
     includes = [INCLUDE, os.path.join(tdir, "include"), os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
