@@ -56,7 +56,9 @@ def build_binding(force: bool = False, verbose: bool = False):
     try:
         import torch
     except ImportError:
-        print("torch is not installed: the native binding of the 4-bit functions is not built", file=sys.stderr)
+        torch = None
+    if torch is None or torch.version.cuda is None:
+        print("torch is not installed, or without CUDA: the native binding of the 4-bit functions is not built", file=sys.stderr)
         return None
     tdir = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"))

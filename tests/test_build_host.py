@@ -34,3 +34,10 @@ def test_the_binding_is_built_where_torch_is(elsewhere):
     assert [c[0] for c in elsewhere] == ["g++"] and os.path.exists(build.BINDING)
     build.build()
     assert len(elsewhere) == 1  # it is up to date
+
+
+def test_a_torch_without_cuda_is_none(elsewhere, monkeypatch, capfd):
+    import torch
+    monkeypatch.setattr(torch.version, "cuda", None)
+    assert build.build() == build.LIB
+    assert not elsewhere and "binding" in capfd.readouterr().err
