@@ -51,20 +51,26 @@ def up_to_date() -> bool:
 
 def build_binding(force: bool = False, verbose: bool = False):
     """Builds the binding; without torch there is nothing to bind to, and the C library is complete by itself."""
-    if not force and newer(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "bitnet_b200.h")]):
-        return BINDING
     try:
         import torch
     except ImportError:
         torch = None
     if torch is None or torch.version.cuda is None:
-        print("torch is not installed, or without CUDA: the native binding of the 4-bit functions is not built", file=sys.stderr)
+        print("torch is not installed, or without CUDA: the native binding of the 4-bit functions is not built",
+              file=sys.stderr)
         return None
+    # a binding fits one torch and one Python: which ones it was built for stands beside it
+    stamp, fits = BINDING[:-len(".so")] + ".stamp", f"{torch.__version__} {sys.implementation.cache_tag}"
+    if not force and newer(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "bitnet_b200.h")]) and os.path.exists(stamp):
+        with open(stamp, encoding="utf-8") as f:
+            if f.read() == fits:
+                return BINDING
     tdir = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"))
     includes = [INCLUDE, os.path.join(tdir, "include"), os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f'-DBINDING_TORCH="{torch.__version__}"',
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f"-I{i}" for i in includes),
            BINDING_SRC, "-o", BINDING + ".tmp", f"-L{os.path.join(tdir, 'lib')}", "-ltorch_python", "-ltorch",
            "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", f"-L{PKG}", "-l:libbitnet_b200.so", "-Wl,-rpath,$ORIGIN"]
@@ -72,6 +78,8 @@ def build_binding(force: bool = False, verbose: bool = False):
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(BINDING + ".tmp", BINDING)
+    with open(stamp, "w", encoding="utf-8") as f:
+        f.write(fits)
     return BINDING
 
 

@@ -310,4 +310,19 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding(void) { return PyModule_Create(&g_module); }
+// Refuses a torch other than the one it was built for: their classes may differ
+// where their symbols do not.
+PyMODINIT_FUNC PyInit__binding(void) {
+    PyObject *torch = PyImport_ImportModule("torch");
+    PyObject *version = torch != nullptr ? PyObject_GetAttrString(torch, "__version__") : nullptr;
+    const char *is = version != nullptr ? PyUnicode_AsUTF8(version) : nullptr;
+    const bool fits = is != nullptr && std::string(is) == BINDING_TORCH;
+    if (is != nullptr && !fits)
+        PyErr_Format(PyExc_ImportError,
+                     "the binding was built for torch " BINDING_TORCH ", this is %s: build it again with "
+                     "`python -m ternary_weight_bit_w2a8_b200.build`",
+                     is);
+    Py_XDECREF(version);
+    Py_XDECREF(torch);
+    return fits ? PyModule_Create(&g_module) : nullptr;
+}

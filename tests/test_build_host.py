@@ -41,3 +41,32 @@ def test_a_torch_without_cuda_is_none(elsewhere, monkeypatch, capfd):
     monkeypatch.setattr(torch.version, "cuda", None)
     assert build.build() == build.LIB
     assert not elsewhere and "binding" in capfd.readouterr().err
+
+
+@pytest.mark.parametrize("name,value", [("torch", "0.1"), ("python", "cpython-27")])
+def test_another_torch_or_python_needs_another_binding(elsewhere, monkeypatch, name, value):
+    import torch
+    build.build()
+    assert len(elsewhere) == 1
+    if name == "torch":
+        monkeypatch.setattr(torch, "__version__", value)
+    else:
+        monkeypatch.setattr(sys.implementation, "cache_tag", value)
+    build.build()
+    assert len(elsewhere) == 2
+    build.build()
+    assert len(elsewhere) == 2
+
+
+def test_a_binding_of_another_torch_is_not_loaded():
+    """In a process of its own: the module refuses to be initialised, and says why."""
+    import subprocess
+    from conftest import ROOT
+    build.build()
+    code = ("import torch\ntorch.__version__ = '0.1'\n"
+            "import ternary_weight_bit_w2a8_b200 as bn\n"
+            "try:\n    bn.bitnet_fp4_quant(torch.zeros(1, 4), 0)\n"
+            "except ImportError as e:\n    print('refused:', e)\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert r.stdout.startswith("refused:") and "0.1" in r.stdout and "build" in r.stdout
