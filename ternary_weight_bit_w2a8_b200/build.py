@@ -34,7 +34,7 @@ NVCC_FLAGS = [
 
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-                  + [os.path.join(INCLUDE, "bitnet_b200.h")])
+                  + glob.glob(os.path.join(CSRC, "*.h")) + [os.path.join(INCLUDE, "bitnet_b200.h")])
 
 
 def newer(target, inputs) -> bool:

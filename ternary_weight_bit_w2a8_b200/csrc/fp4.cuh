@@ -16,10 +16,10 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "fp4_plan.h"
 
 namespace bitnet {
 
-constexpr int kFp4TileRows = 128;   // rows of a scale tile
 constexpr int kFp4TileBytes = 512;  // 128 rows x 4 blocks, one byte each
 
 __host__ __device__ __forceinline__ int fp4_block(int format) { return format == BITNET_FP4_MX ? 32 : 16; }
@@ -289,8 +289,6 @@ __device__ __forceinline__ uint32_t fp4_codes8(const uint64_t (&x)[4], float inv
 // 5120 bf16 36.3, 34.1 and 36.1.
 //   ALIGNED: rows of x start on 16-byte boundaries.  Otherwise a warp reads a
 // row's values in order, one to a lane, and shared memory turns them round.
-constexpr int kFp4PatchK = 256;
-
 template <int DT, int FMT, bool ALIGNED, int ROWS>
 __global__ void __launch_bounds__(kThreads) fp4_quant_kernel(const typename Fp4Type<DT>::T *__restrict__ x,
                                                              int64_t rows, int64_t K, int64_t ldx,

@@ -16,10 +16,7 @@
 
 namespace bitnet {
 
-constexpr int kFp4Rows = 128;     // rows of the P operand per tile (UMMA M)
-constexpr int kFp4StageK = 256;   // k per stage: a 128-byte swizzled row of codes
 constexpr int kFp4Threads = 192;  // producer, MMA issuer, 4 epilogue (and quantiser) warps
-constexpr int kFp4MaxSplit = 8;   // largest portable cluster
 constexpr int kFp4FusedTokens = 16;
 constexpr int kFp4Prefetch = 4;  // stages of weights asked into L2 before the launch-chain wait
 
