@@ -140,3 +140,18 @@ def test_dequant_in_patches_of_64_rows(fmt, dt, rows, K, behind):
     out.check("y")
     assert torch.equal(out.t[:, :K], want)
     assert bool((out.t[:, K:] == 5.0).all())
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M", [5, 40, 100])
+def test_layer_of_tokens_that_are_not_finite(fmt, M):
+    """A token with a NaN or an infinity gives NaN, and the others what they give without it."""
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    x = torch.randn(M, 700, device="cuda", generator=gen).to(torch.bfloat16)
+    w, w_s = bn.bitnet_fp4_quant(torch.randn(300, 700, device="cuda", generator=gen), fmt)
+    clean = bn.bitnet_fp4_linear(x, w, w_s, fmt)
+    x[1, 699], x[4, 0] = float("nan"), float("-inf")
+    y = bn.bitnet_fp4_linear(x, w, w_s, fmt)
+    assert bool(y[[1, 4]].isnan().all())
+    rest = [m for m in range(M) if m not in (1, 4)]
+    assert torch.equal(y[rest], clean[rest])
