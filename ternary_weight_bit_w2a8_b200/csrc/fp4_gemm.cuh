@@ -42,19 +42,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_flag)) != 0;
 }
 
-// Before a CTA leaves: whole-warp bounded wait for the arrivals of the MMAs that
-// emptied the last of its n stages, a lane to each.  They come by commits of
-// their own, and nothing says that those arrive before the accumulator's, later
-// one.  (Where CTAs exchange sums the wait comes after that: before it, it kept
-// 1 x 2560 x 6912 0.3 us longer.)
-template <int S>
-__device__ __forceinline__ void wait_last_empty(uint64_t *empty, int n, int lane, volatile int *abort_flag) {
-    static_assert(S <= 32, "a lane to each");
-    const int j = n - 1 - lane;
-    if (lane < S && j >= 0) tc_wait(&empty[j % S], (uint32_t)(j / S) & 1u, abort_flag);
-    __syncwarp();
-}
-
 // Instruction descriptor: e2m1 x e2m1, fp32 accumulate, K-major, M = m, N = n,
 // scale type 1 (e8m0) or 0 (e4m3); the two scale ids (which byte of a column
 // holds the first scale) are added per instruction.
@@ -399,7 +386,8 @@ __global__ void __launch_bounds__(kFp4Threads, Fp4Small<FMT, BT>::kCtas)
                         umma_fp4<FMT>(tmem, w0 + at + 2 * j, a0 + at + 2 * j, idesc | fp4_scale_id(id), cw + 4 * t,
                                       ca + 4 * t, j > 0 ? 1u : (uint32_t)(i > 0));
                 }
-                umma_commit(&empty[s]);
+                // (an arrival that no load waits for could come after the CTA has left)
+                if (i + S < n_i) umma_commit(&empty[s]);
                 if (++s == S) s = 0, phase ^= 1;
             }
             umma_commit(ok ? done : drain);
@@ -455,10 +443,8 @@ __global__ void __launch_bounds__(kFp4Threads, Fp4Small<FMT, BT>::kCtas)
             for (int i = 0; i < 4; ++i)
                 if (n + i < a.N) fp4_store(a.y, c * a.ldy + n + i, fp4_scaled(o[i], g), a.ytype);
         }
-        if (warp == 1 && !*abort_flag) wait_last_empty<S>(empty, n_i, lane, abort_flag);
         cluster_sync_relaxed();  // nobody reads this CTA's shared memory any more
     } else {
-        if (warp == 1 && !*abort_flag) wait_last_empty<S>(empty, n_i, lane, abort_flag);
         __syncthreads();
     }
     if (warp == 1) {

@@ -106,13 +106,13 @@ __device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t des
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-// Arrives on the barrier at this offset in both CTAs (`lead` is the cluster rank
-// of the first) once the tensor-core work issued so far is done.
-__device__ __forceinline__ void umma_commit_pair(uint64_t *bar, uint32_t lead) {
+// Arrives on the barrier at this offset in both CTAs (or the first alone; `lead`
+// is its cluster rank) once the tensor-core work issued so far is done.
+__device__ __forceinline__ void umma_commit_pair(uint64_t *bar, uint32_t lead, uint32_t ctas = 3u) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_u32(bar)),
-        "h"((uint16_t)(3u << lead))
+        "h"((uint16_t)(ctas << lead))
         : "memory");
 }
 
@@ -389,7 +389,6 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
         // sees both CTAs' copies; they leave together)
         if (rank == 0)
             for (int j = g - S < 0 ? 0 : g - S; j < g; ++j) mbar_wait_bounded(&full[j % S], (uint32_t)(j / S) & 1u);
-        if (!SPLIT && ok) wait_last_empty<S>(empty, g, lane, abort_flag);
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
         // One thread; what it does per stage has to stay below the MMAs' 2 BT cycles.
@@ -399,6 +398,7 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
             const uint64_t a0 = umma_desc_sw128(base), w0 = umma_desc_sw128(base + L::kABytes);
             const uint64_t s0 = scale_desc(base + L::kABytes + L::kWBytes);
             const int full_stages = (int)(kp / kFp4StageK);  // the last stage may hold 128 k only
+            const int total = (SPLIT ? 1 : (units - pair + pairs - 1) / pairs) * (nk - k0);  // stages of this pair's tiles
             bool ok = true;
             int s = 0, slot = 0, g = 0, li = 0;
             uint32_t phase = 0;
@@ -454,7 +454,12 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
                         if (i == k0 && !(ok = acc_free(1, li))) break;
                         multiply(1);
                     }
-                    umma_commit_pair(&empty[s], lead);
+                    // Only for those who wait: the producers for the stage S further on, this thread for the one kSlots
+                    // further on.  (Any other arrival could come after its CTA has left.)
+                    if (g + S < total)
+                        umma_commit_pair(&empty[s], lead);
+                    else if (L::kSlots < S && g + L::kSlots < total)
+                        umma_commit_pair(&empty[s], lead, 1u);
                     if (++s == S) s = 0, phase ^= 1;
                     if (++slot == L::kSlots) slot = 0;
                 }
@@ -571,7 +576,6 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
                     if (n + i < a.N) fp4_store(a.y, m * a.ldy + n + i, v[i], a.ytype);
             }
         }
-        if (warp == 1 && !*abort_flag) wait_last_empty<S>(empty, nk - k0, lane, abort_flag);
     }
     __syncthreads();
     cluster_sync_relaxed();  // neither CTA signals the other or reads its shared memory any more
