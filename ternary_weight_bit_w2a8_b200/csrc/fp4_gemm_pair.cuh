@@ -501,8 +501,9 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
                 }
             }
         }
-        // waits for use `use` of accumulator d, reads this warp's part of it as 16-bit pairs and releases it
-        auto empty_acc = [&](int d, int use, uint32_t (&v)[16 * kMost]) -> bool {
+        // waits for use `use` of accumulator d, reads this warp's part of it as 16-bit pairs and releases it (where it is
+        // used again: any other arrival could come after the first CTA has left)
+        auto empty_acc = [&](int d, int use, bool again, uint32_t (&v)[16 * kMost]) -> bool {
             if (!warp_wait(&acc_full[d], (uint32_t)use & 1u, abort_flag)) return false;
             tc_fence_after();
             uint32_t f[32 * kMost];
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&acc_empty[d]), lead));
+            if (again && lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&acc_empty[d]), lead));
             if (a.ytype == BITNET_FP16)
                 pack_all<BITNET_FP16, L::kHalves == 2>(v, f, gs);
             else
@@ -535,12 +536,13 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
             const int64_t n0 = (int64_t)(u / a.tiles_m) * BT + part * kMost * 32;
             uint32_t v[16 * kMost];
             if constexpr (L::kHalves == 1) {
-                if (!empty_acc(li & 1, li >> 1, v)) break;
+                if (!empty_acc(li & 1, li >> 1, units - u > 2 * pairs, v)) break;
                 store(m0, n0, v);
             } else {
                 // both halves are emptied before the first is stored: the next tile waits for them
                 uint32_t v1[16 * kMost];
-                if (!empty_acc(0, li, v) || !empty_acc(1, li, v1)) break;
+                const bool again = units - u > pairs;
+                if (!empty_acc(0, li, again, v) || !empty_acc(1, li, again, v1)) break;
                 store(m0, n0, v);
                 store(m0, n0 + L::kCols, v1);
             }

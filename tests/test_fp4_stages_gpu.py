@@ -42,3 +42,25 @@ def test_every_number_of_stages(fmt, call, M, N):
         want, mag = av @ wv.t(), av.abs() @ wv.abs().t()
         tol = want.abs() * 2.0 ** -8 + mag * (K / 16 + 16) * 2.0 ** -22  # half a step of bf16, and the fp32 sums'
         assert bool(((y.double() - want).abs() <= tol).all()), stages
+
+
+@pytest.mark.parametrize("fmt", [bn.BITNET_FP4_MX, bn.BITNET_FP4_NV])
+@pytest.mark.parametrize("N", [64, 128, 192, 256, 384])
+def test_every_number_of_tiles(fmt, N):
+    """One, two and three tiles to a pair of the 74, and one pair with one more: which uses of the accumulators are
+    handed back."""
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    for K in (128, 1300):
+        w, ws = bn.bitnet_fp4_quant(torch.randn(N, K, device="cuda", generator=gen), fmt)
+        wv = bn.bitnet_fp4_dequant(w, ws, K, fmt, dtype=torch.float32).double()
+        for tiles in (1, 73, 74, 75, 147, 148, 149, 222, 223):
+            M = 256 * tiles - 100
+            a, sa = bn.bitnet_fp4_quant(torch.randn(M, K, device="cuda", generator=gen), fmt)
+            av = bn.bitnet_fp4_dequant(a, sa, K, fmt, dtype=torch.float32).double()
+            want, mag = av @ wv.t(), av.abs() @ wv.abs().t()
+            tol = want.abs() * 2.0 ** -8 + mag * (K / 16 + 16) * 2.0 ** -22
+            for behind in (0, 1):
+                y = torch.empty(M, N + behind, dtype=torch.bfloat16, device="cuda")[:, :N]
+                bn.bitnet_fp4_gemm(a, sa, w, ws, K, fmt, y=y)
+                assert bn.bitnet_get_device_error() == bn.BITNET_OK, (K, tiles)
+                assert bool(((y.double() - want).abs() <= tol).all()), (K, tiles)
