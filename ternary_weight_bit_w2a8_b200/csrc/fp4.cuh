@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(kThreads) fp4_dequant_kernel(const uint8_t *__
 // to 0 by a launch before.  What kFp4ScaleCluster CTAs take in one round of
 // loads (256 KB) is one cluster instead: the first CTA reads the others' values
 // and stores g, and there is no launch before (16 x 2560 bf16: 3.6 us of host
-// time and 2.9 of the GPU's, not 5.9 and 2.4).  A warp takes a piece of a
+// time and 2.5 of the GPU's, not 5.9 and 2.4).  A warp takes a piece of a
 // row at a time, four 32-byte loads to a lane; the values before the row's
 // first 32-byte boundary and behind its last are taken one by one.
 __global__ void fp4_clear_kernel(float *g) {
@@ -615,25 +615,26 @@ __global__ void __launch_bounds__(kThreads, 4) fp4_tensor_scale_kernel(const typ
     }
     top = block_reduce(top, [](uint32_t a, uint32_t b) { return a > b ? a : b; }, red);
     const bool cluster = gridDim.x <= kFp4ScaleCluster;  // launched as one
+    __shared__ uint32_t mine;
     if (cluster && gridDim.x > 1) {
-        __shared__ uint32_t mine;
         if (threadIdx.x == 0) mine = top;
         cluster_sync();
-        if (blockIdx.x == 0)
+    }
+    if (threadIdx.x == 0 && !(cluster && blockIdx.x > 0)) {
+        if (cluster)
             for (uint32_t r = 1; r < gridDim.x; ++r) {
                 const uint32_t t = ld_cluster_u32(map_rank((uint32_t)__cvta_generic_to_shared(&mine), r));
                 top = t > top ? t : top;
             }
-        cluster_sync_relaxed();  // nobody leaves while its value may be read
-    }
-    if (threadIdx.x == 0) {
         const float v = __fdiv_rn(__uint_as_float(top), 2688.0f);
         const float s = v > 1.17549435e-38f ? v : 1.17549435e-38f;
-        if (!cluster)
-            atomicMax(reinterpret_cast<uint32_t *>(g), __float_as_uint(s));
-        else if (blockIdx.x == 0)
+        if (cluster)
             *g = s;
+        else
+            atomicMax(reinterpret_cast<uint32_t *>(g), __float_as_uint(s));
     }
+    // nobody leaves while its value may be read (g has been stored from them before the reader arrives)
+    if (cluster && gridDim.x > 1) cluster_sync_relaxed();
 }
 
 }  // namespace bitnet

@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(kFp4Threads, Fp4Small<FMT, BT>::kCtas)
         for (int e = threadIdx.x; e < a.M * quads; e += kFp4Threads) {
             const int c = e / quads, row = r0 + 4 * (e % quads);
             const int64_t n = (int64_t)tile * kFp4Rows + row;
+            if (n >= a.N) continue;  // (what is read is stored: no read is still under way at the barrier below)
             const uint32_t at = base + (uint32_t)(c * kFp4Rows + row) * 4;
             float4 v[kFp4MaxSplit];
 #pragma unroll

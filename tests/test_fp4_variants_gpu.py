@@ -155,3 +155,18 @@ def test_layer_of_tokens_that_are_not_finite(fmt, M):
     assert bool(y[[1, 4]].isnan().all())
     rest = [m for m in range(M) if m not in (1, 4)]
     assert torch.equal(y[rest], clean[rest])
+
+
+@pytest.mark.parametrize("dt", list(TYPES))
+def test_tensor_scale_of_every_cluster(dt):
+    """One to eight CTAs of a cluster, and more without one, each holding the largest value once."""
+    per_cta = (8 if dt == "fp32" else 16) * 32 * 4 * 8  # values that a CTA's eight warps take at once
+    for ctas in (1, 2, 3, 5, 7, 8, 9, 12):
+        n = ctas * per_cta - 5
+        x = torch.full((1, n), 0.5, dtype=TYPES[dt], device="cuda")
+        for at in range(0, n, per_cta):
+            x[0, at + 3] = -(2.0 + at / per_cta)
+            got = bn.bitnet_fp4_tensor_scale(x)
+            x[0, at + 3] = 0.5
+            want = np.float32(2.0 + at / per_cta) / np.float32(2688)
+            assert got.item() == want, (ctas, at)
