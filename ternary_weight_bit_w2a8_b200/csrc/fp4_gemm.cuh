@@ -17,6 +17,12 @@
 namespace bitnet {
 
 constexpr int kFp4Threads = 192;  // producer, MMA issuer, 4 epilogue (and quantiser) warps
+// Tokens that are quantised inside the product's launch; callers count on needing
+// no workspace up to there.  In a graph, one launch against quantising first: 1
+// token 4.9 to 6.7 us and 6.1 to 7.7 for 2560 x 6912 to 13824 x 2560, 16 tokens
+// 6.7 to 8.2 and 6.7 to 8.8.  But every CTA quantises all tokens of its range of
+// k: with 27648 rows and more one token takes as long either way, and 4 to 16
+// take longer (55296 x 5120 MX: 28.6 to 33.4 us, quantised first 25.8 to 26.5).
 constexpr int kFp4FusedTokens = 16;
 constexpr int kFp4Prefetch = 4;  // stages of weights asked into L2 before the launch-chain wait
 

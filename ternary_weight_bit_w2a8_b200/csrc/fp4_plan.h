@@ -67,7 +67,12 @@ inline int fp4_split(int64_t M, int64_t N, int64_t K) {
 // share a tile (clusters of 4 or 8 CTAs, which fill some 64 pairs' SMs at once)
 // for an exchange of some kExchange ns: 100 x 500 x 20000 MX takes 21.6 us with
 // one pair to a tile, 12.3 with two, 8.3 with four; 448 x 1664 x 18022 19.4
-// with one, 14.7 with two and 128 rows.
+// with one, 14.7 with two and 128 rows.  (77 x 3211 x 4801 NV, two pairs and 10
+// stages each, takes 8.6, with half that k 7.6, with 512 k and one pair to a
+// tile 3.3: a shared tile costs some 3 us beside its stages, which kExchange
+// does not count.)
+//   The numbers of pairs are the B200's and not the device's, so that the split,
+// and with it the sums, are the same wherever the library runs.
 struct Fp4PairPlan {
     int width, split;
 };
