@@ -240,8 +240,9 @@ def bitnet_w2a8_gemm_noalloc(q, packed, N: int, y=None, stream=None):
 
 # ------------------------------------------------------------------ 4-bit floating point
 # The tensors of a call lie on one CUDA device, which need not be the current
-# one; x and y may be row-strided views, everything else is contiguous.  The
-# checks and the marshalling of these calls are native (csrc/binding.cpp).
+# one; x and y may be row-strided views, everything else is contiguous.  A scale
+# (g, ga, gw) is a float32 tensor of one value, dtype that of y if both are given.
+# The checks and the marshalling of these calls are native (csrc/binding.cpp).
 
 _native = None
 

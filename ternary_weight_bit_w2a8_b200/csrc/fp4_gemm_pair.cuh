@@ -467,8 +467,9 @@ __global__ void __launch_bounds__(kFp4PairThreads, 1)
                 umma_commit_pair(&acc_full[L::kHalves == 2 ? 1 : d], lead);
             }
             if (!ok) {
-                // the MMAs issued so far end before tensor memory is freed
-                umma_commit_pair(drain, lead);
+                // the MMAs issued so far end before tensor memory is freed (only this CTA waits for them, and the other
+                // for this one)
+                umma_commit_pair(drain, lead, 1u);
                 mbar_wait_bounded(drain, 0);
             }
         }
